@@ -354,6 +354,142 @@ pa_status pa_decode_step(const pa_config *cfg, int32_t batch, const int32_t *kv_
 pa_status pa_attend_noalloc(const pa_plan *plan, const void *q, const void *k_pool, const void *v_pool, void *out,
                             float *lse, void *stream);
 
+/*
+ * ------------------------------------------------------------------ session caches on the device
+ *
+ * The calls below work on a batch of sessions whose lengths and block tables
+ * live on the device, so that one captured CUDA graph serves every step: they
+ * plan nothing on the host and read nothing back.  They fill (pa_rope_append),
+ * read (pa_window_attend), weigh (pa_weigh_tokens) and prune (pa_evict_tokens)
+ * the paged cache of stateful sessions (the stateful-streaming summary,
+ * 方法拆解: a session's KV persists and is advanced as data arrives).
+ *
+ *   n_sessions       S in 1 .. 65535
+ *   num_rows         rows of q (0 allowed: nothing is done); rows of session s
+ *                    are [cu_rows[s], cu_rows[s + 1]), none allowed
+ *   num_q_heads, num_kv_heads, head_dim, page_size
+ *                    as in pa_config (Hq / Hkv 1, 2, 4 or 8; D 64 or 128; P 16)
+ *   max_pages        width of the block table
+ *   num_pages_in_pool
+ *                    first dimension of the pools
+ *   d_block_table    device int32 [S][max_pages]
+ *   d_kv_lens        device int32 [S]: cached tokens, the session's rows among
+ *                    them (0 allowed; taken as at most max_pages * P)
+ *   d_cu_rows        device int32 [S + 1], ascending from 0; rows at or past
+ *                    cu_rows[S] belong to no session and their outputs are left
+ *                    as they were.  pa_evict_tokens does not read it (NULL).
+ * The i-th of the n rows of a session is its cached token kv_len - n + i (its
+ * position).  A block-table entry outside [0, num_pages_in_pool) is a hole: its
+ * tokens are neither written, seen nor copied.  Cached tokens of a session
+ * hold finite K and V; slots at or past kv_len may hold anything.
+ * The device arrays are read when the kernels run.  Arguments are checked
+ * before anything is enqueued: PA_ERR_INVALID for a null or misaligned pointer
+ * (q, k, v, pools, outputs: 16 bytes) or a bad size, PA_ERR_UNSUPPORTED for a
+ * head layout, head_dim or page size that is not built or a pool beyond 2^31 - 1
+ * (page, head, slot) rows, PA_ERR_CUDA when a launch fails.  All are asynchronous on
+ * `stream` of the current device, keep nothing between calls and are bit
+ * reproducible.
+ */
+typedef struct {
+  int32_t n_sessions, num_rows;
+  int32_t num_q_heads, num_kv_heads, head_dim, page_size;
+  int32_t max_pages, num_pages_in_pool;
+  const int32_t *d_block_table;
+  const int32_t *d_kv_lens;
+  const int32_t *d_cu_rows;
+} pa_sessions;
+
+/*
+ * Rotary positions: pair i of a head's first rotary_dim dims turns by
+ * positions[axes[i]][r] * inv_freq[i], (x, y) -> (x cos - y sin, x sin + y cos).
+ * Several axes (time, height, width) give each frequency its own coordinate.
+ *   rotary_dim    R: a multiple of 16, at most head_dim; the rest is copied
+ *   n_axes        1 .. 4
+ *   interleaved   0: pair i is dims (i, i + R/2); 1: dims (2i, 2i + 1)
+ *   axes          host uint8 [R / 2]: axis of each pair; NULL: all axis 0.  Read
+ *                 during the call only
+ *   d_positions   device int32 [n_axes][num_rows]
+ *   d_inv_freq    device fp64 [R / 2], radians per position
+ */
+typedef struct {
+  int32_t rotary_dim, n_axes, interleaved;
+  const uint8_t *axes;
+  const int32_t *d_positions;
+  const double *d_inv_freq;
+} pa_rope;
+
+/*
+ * Append: rotates q and k (angles reduced in fp64, one rounding to bf16) and
+ * writes each row's k and v into its slot of the pools.
+ *   q, k, v       device bf16 [num_rows][heads][D], heads contiguous, rows
+ *                 *_row_stride elements apart (a multiple of 8): they may be
+ *                 slices of one projection's output
+ *   q_out         device bf16 [num_rows][Hq][D]; may be q itself when q's rows
+ *                 are contiguous
+ * A row whose position is negative or whose page is a hole is rotated in q_out
+ * and written nowhere else.  Two rows of one slot (a page held by two sessions
+ * that both write it) race.
+ */
+pa_status pa_rope_append(const pa_sessions *b, const pa_rope *rope, const void *q, int64_t q_row_stride,
+                         const void *k, int64_t k_row_stride, const void *v, int64_t v_row_stride, void *k_pool,
+                         void *v_pool, void *q_out, void *stream);
+
+/* Device workspace (256-byte aligned) that pa_window_attend needs for any
+ * contents of the device arrays.  A workspace holds nothing between calls;
+ * calls that may overlap on the GPU need one each. */
+pa_status pa_window_workspace_size(const pa_sessions *b, int32_t window, int32_t sinks, size_t *bytes);
+
+/*
+ * Attend: every row over its session's cache, causal, with a sliding window
+ * and sinks.  The row at position p sees token t when t <= p and
+ * (window == 0 or t > p - window or t < sinks).
+ *   window, sinks     >= 0; window 0: no limit
+ *   softmax_scale     0 selects 1 / sqrt(D)
+ *   q                 device bf16 [num_rows][Hq][D]
+ *   out               device bf16 [num_rows][Hq][D]
+ *   lse               device fp32 [num_rows][Hq], natural log; may be NULL
+ * A row that sees nothing gets zeros and lse = -inf.  PA_ERR_NOMEM when
+ * workspace_bytes is below pa_window_workspace_size.
+ */
+pa_status pa_window_attend(const pa_sessions *b, int32_t window, int32_t sinks, float softmax_scale, const void *q,
+                           const void *k_pool, const void *v_pool, void *d_workspace, size_t workspace_bytes,
+                           void *out, float *lse, void *stream);
+
+/*
+ * Weigh: adds to scores the attention weight that every cached token draws from the
+ * batch's rows,
+ *   scores[s][g][t] += sum_{rows r of s that see t, heads h of g} e^{scale q_rh . k_t - lse_rh},
+ * with pa_window_attend's lse, window, sinks and scale.
+ *   scores            device fp32 [S][Hkv][max_tokens]; tokens at or past
+ *                     max_tokens are not recorded; entries at or past kv_len
+ *                     are left as they were
+ * A row with lse = -inf (one that sees nothing) weighs nothing.
+ */
+pa_status pa_weigh_tokens(const pa_sessions *b, int32_t window, int32_t sinks, float softmax_scale, const void *q,
+                          const void *k_pool, const float *lse, float *scores, int64_t max_tokens, void *stream);
+
+/*
+ * Evict: every (session, kv head) keeps its first `sinks` and last `recent`
+ * tokens and the highest-scoring of the rest, `budget` tokens in all (all of
+ * them when there are no more); equal scores keep the lower index, NaN ranks
+ * above every number.  The kept tokens go, in order, to the session's row of
+ * the destination table, each kv head its own tokens: the result is an
+ * ordinary paged cache of min(kv_len, budget) tokens.
+ *   scores            device fp32 [S][Hkv][max_tokens] (as pa_weigh_tokens);
+ *                     kv_len is taken as at most max_tokens
+ *   d_dst_table       device int32 [S][dst_max_pages], dst_max_pages * P >=
+ *                     budget.  Destination pages must not be pages that the
+ *                     block table names (a copy would race with a read)
+ *   scores_out        device fp32 [S][Hkv][max_tokens], not scores: the kept
+ *                     tokens' scores, then zeros
+ *   kept              device int32 [S][Hkv][budget]: the kept tokens' former
+ *                     indices, ascending, then -1
+ *   new_lens          device int32 [S]
+ */
+pa_status pa_evict_tokens(const pa_sessions *b, const float *scores, int64_t max_tokens, void *k_pool, void *v_pool,
+                          const int32_t *d_dst_table, int32_t dst_max_pages, int32_t budget, int32_t sinks,
+                          int32_t recent, float *scores_out, int32_t *kept, int32_t *new_lens, void *stream);
+
 /* Release a plan (NULL is ignored). */
 void pa_plan_destroy(pa_plan *plan);
 

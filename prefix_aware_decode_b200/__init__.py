@@ -7,3 +7,14 @@ from ._binding import (PA_ERR_CUDA, PA_ERR_DEVICE, PA_ERR_INVALID, PA_ERR_NOMEM,
                        PA_ERR_UNSUPPORTED, PA_OK, PA_PLAN_ALWAYS_SHARE, PA_PLAN_DEBUG_CHECKS,
                        PA_PLAN_FAULT_DROP_LOAD, PA_PLAN_KEEP_PACK, PA_PLAN_NO_SHARING, DecodeStep, PaError, PaImageHeader, Plan, attend, merge_rows,
                        lib)
+
+_CACHE_OPS = ("evict_tokens", "rope_append", "weigh_tokens", "window_attend", "window_workspace")
+
+
+def __getattr__(name):
+    # the session-cache operators take torch tensors: imported with torch at their first use
+    if name in _CACHE_OPS:
+        from . import cache_ops
+        globals().update({n: getattr(cache_ops, n) for n in _CACHE_OPS})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -63,10 +63,22 @@ class PaImageHeader(ctypes.Structure):
                                                   "workspace_bytes")])
 
 
+class PaSessions(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("n_sessions", "num_rows", "num_q_heads", "num_kv_heads", "head_dim",
+                                               "page_size", "max_pages", "num_pages_in_pool")]
+                + [(n, ctypes.c_void_p) for n in ("d_block_table", "d_kv_lens", "d_cu_rows")])
+
+
+class PaRope(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("n_axes", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("axes", ctypes.c_char_p), ("d_positions", ctypes.c_void_p), ("d_inv_freq", ctypes.c_void_p)]
+
+
 # exported names, in the order pa.h declares them
 EXPORTS = ["pa_plan_create", "pa_plan_advance", "pa_plan_create_append", "pa_plan_workspace_size", "pa_plan_upload", "pa_forward", "pa_merge", "pa_merge_f32", "pa_merge_rows", "pa_attend",
            "pa_get_device_status", "pa_plan_get_stats", "pa_plan_host_image", "pa_plan_set_profile_events",
-           "pa_decode_step", "pa_attend_noalloc", "pa_plan_destroy", "pa_status_string"]
+           "pa_decode_step", "pa_attend_noalloc", "pa_rope_append", "pa_window_workspace_size", "pa_window_attend",
+           "pa_weigh_tokens", "pa_evict_tokens", "pa_plan_destroy", "pa_status_string"]
 
 _lib = None
 
@@ -114,6 +126,17 @@ def lib() -> ctypes.CDLL:
     L.pa_decode_step.restype = st
     L.pa_attend_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp]
     L.pa_attend_noalloc.restype = st
+    i64, f32, sp = ctypes.c_int64, ctypes.c_float, ctypes.POINTER(PaSessions)
+    L.pa_rope_append.argtypes = [sp, ctypes.POINTER(PaRope), vp, i64, vp, i64, vp, i64, vp, vp, vp, vp]
+    L.pa_rope_append.restype = st
+    L.pa_window_workspace_size.argtypes = [sp, i32, i32, ctypes.POINTER(sz)]
+    L.pa_window_workspace_size.restype = st
+    L.pa_window_attend.argtypes = [sp, i32, i32, f32, vp, vp, vp, vp, sz, vp, vp, vp]
+    L.pa_window_attend.restype = st
+    L.pa_weigh_tokens.argtypes = [sp, i32, i32, f32, vp, vp, vp, vp, i64, vp]
+    L.pa_weigh_tokens.restype = st
+    L.pa_evict_tokens.argtypes = [sp, vp, i64, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp]
+    L.pa_evict_tokens.restype = st
     L.pa_plan_destroy.argtypes = [vp]
     L.pa_plan_destroy.restype = None
     L.pa_status_string.argtypes = [st]

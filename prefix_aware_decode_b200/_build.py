@@ -20,9 +20,9 @@ BUILD = os.path.join(REPO, "_build")
 LIB = os.path.join(HERE, "libpa.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
-CU_SOURCES = ["kernels.cu", "capi.cu", "noalloc.cu"]
+CU_SOURCES = ["kernels.cu", "capi.cu", "noalloc.cu", "rope_append.cu", "window_attend.cu", "weigh.cu", "evict.cu"]
 CPP_SOURCES = ["plan.cpp"]
-HEADERS = ["plan.h", "ptx.cuh"]
+HEADERS = ["plan.h", "ptx.cuh", "sessions.cuh"]
 
 
 def nvcc() -> str:

@@ -1,0 +1,162 @@
+// Rotary positions with several axes, fused with the write of new K and V rows
+// into their pages (pa_rope_append).
+//
+// Pair i of a head turns by angle(r, i) = positions[axis(i)][r] * inv_freq[i]:
+// (x, y) -> (x cos - y sin, x sin + y cos).  The angle is formed and reduced to
+// half turns in fp64: at position 2^20 an fp32 product would be off by 2^-4
+// radian, the fp64 one by 2^-33.  One sincospif per (row, pair), shared by all
+// heads of the row through shared memory; the rotation itself is fp32, rounded
+// to bf16 once.
+//
+// Bound by memory: each q, k, v element is read and written once.
+#include "ptx.cuh"
+#include "sessions.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kRopeThreads = 256;
+
+struct RopeArgs {
+  Sessions b;
+  const uint16_t *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;  // elements from row to row
+  const int32_t* positions;              // [n_axes][rows]
+  const double* inv_freq;                // [R / 2]
+  uint16_t *k_pool, *v_pool, *q_out;
+  int R, interleaved;
+  uint32_t axes[4];  // 2 bits per pair: its axis
+};
+
+// ROWS consecutive rows per CTA.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArgs a) {
+  __shared__ float2 turn[ROWS][D / 2];  // (cos, sin)
+  __shared__ long long slot[ROWS];      // pool offset of the row's kv head 0 slot; -1: none
+  __shared__ int live[ROWS];            // the row belongs to a session
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r0 = blockIdx.x * ROWS;
+  const int pairs = a.R >> 1;
+  for (int i = tid; i < ROWS * pairs; i += kRopeThreads) {
+    const int j = i / pairs, p = i - j * pairs, r = r0 + j;
+    if (r < a.b.rows) {
+      const int axis = (a.axes[p >> 4] >> (2 * (p & 15))) & 3;
+      const double half_turns =
+          (double)a.positions[(size_t)axis * a.b.rows + r] * a.inv_freq[p] * 0.31830988618379067154;
+      float s, c;
+      sincospif((float)(half_turns - 2.0 * rint(0.5 * half_turns)), &s, &c);
+      turn[j][p] = make_float2(c, s);
+    }
+  }
+  for (int j = warp; j < ROWS; j += kRopeThreads / 32) {
+    const int r = r0 + j;
+    long long at = -1;
+    int in = 0;
+    if (r < a.b.rows) {
+      const int s = warp_find_session(a.b, r, lane);
+      const int b0 = a.b.row_begin(s), n = a.b.row_begin(s + 1) - b0;
+      in = r >= b0 && r < b0 + n;
+      const int t = a.b.kv_len(s) - n + (r - b0);
+      if (in && t >= 0) {
+        const int page = a.b.page(s, t / kPage);
+        if (page >= 0) at = ((long long)page * a.b.Hkv * kPage + t % kPage) * D;
+      }
+    }
+    if (lane == 0) {
+      slot[j] = at;
+      live[j] = in;
+    }
+  }
+  __syncthreads();
+  // units of 16 elements (two 16-byte vectors) of a head
+  constexpr int U = D / 16;
+  const int Hq = a.b.Hq, Hkv = a.b.Hkv, rot = a.R / 16;
+  const int per_row = (Hq + 2 * Hkv) * U;
+  for (int i = tid; i < ROWS * per_row; i += kRopeThreads) {
+    const int j = i / per_row, x = i - j * per_row, h = x / U, u = x % U, r = r0 + j;
+    if (r >= a.b.rows || !live[j]) continue;
+    const uint16_t* src;
+    uint16_t* dst;
+    const bool is_v = h >= Hq + Hkv;
+    if (h < Hq) {
+      src = a.q + (int64_t)r * a.q_stride + h * D;
+      dst = a.q_out + ((int64_t)r * Hq + h) * D;
+    } else {
+      if (slot[j] < 0) continue;
+      const int g = is_v ? h - Hq - Hkv : h - Hq;
+      src = (is_v ? a.v + (int64_t)r * a.v_stride : a.k + (int64_t)r * a.k_stride) + g * D;
+      dst = (is_v ? a.v_pool : a.k_pool) + slot[j] + (int64_t)g * kPage * D;
+    }
+    // element offsets of the unit's two vectors
+    const bool split = u < rot && !a.interleaved;
+    const int e0 = split ? 8 * u : 16 * u, e1 = split ? e0 + a.R / 2 : e0 + 8;
+    uint4 x0 = *reinterpret_cast<const uint4*>(src + e0), x1 = *reinterpret_cast<const uint4*>(src + e1);
+    if (u < rot && !is_v) {
+      uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
+      const float2* cs = &turn[j][8 * u];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        if (split) {  // pairs (e0 + 2m, e1 + 2m), (e0 + 2m + 1, e1 + 2m + 1)
+          const float2 p = bf16x2_to_f2(w0[m]), y = bf16x2_to_f2(w1[m]);
+          const float2 t0 = cs[2 * m], t1 = cs[2 * m + 1];
+          w0[m] = pack_bf16x2(p.x * t0.x - y.x * t0.y, p.y * t1.x - y.y * t1.y);
+          w1[m] = pack_bf16x2(p.x * t0.y + y.x * t0.x, p.y * t1.y + y.y * t1.x);
+        } else {  // each word is a pair
+          const float2 p = bf16x2_to_f2(w0[m]), y = bf16x2_to_f2(w1[m]);
+          const float2 t0 = cs[m], t1 = cs[4 + m];
+          w0[m] = pack_bf16x2(p.x * t0.x - p.y * t0.y, p.x * t0.y + p.y * t0.x);
+          w1[m] = pack_bf16x2(y.x * t1.x - y.y * t1.y, y.x * t1.y + y.y * t1.x);
+        }
+      }
+      x0 = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+      x1 = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+    }
+    *reinterpret_cast<uint4*>(dst + e0) = x0;
+    *reinterpret_cast<uint4*>(dst + e1) = x1;
+  }
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" pa_status pa_rope_append(const pa_sessions* b, const pa_rope* rope, const void* q, int64_t q_row_stride,
+                                    const void* k, int64_t k_row_stride, const void* v, int64_t v_row_stride,
+                                    void* k_pool, void* v_pool, void* q_out, void* stream) {
+  const pa_status st = pa_check_sessions(b, true);
+  if (st != PA_OK) return st;
+  if (!rope || rope->n_axes < 1 || rope->n_axes > 4 || rope->rotary_dim < 16 || rope->rotary_dim > b->head_dim ||
+      rope->rotary_dim % 16)
+    return PA_ERR_INVALID;
+  if (rope->axes)
+    for (int i = 0; i < rope->rotary_dim / 2; ++i)
+      if (rope->axes[i] >= rope->n_axes) return PA_ERR_INVALID;
+  if (b->num_rows == 0) return PA_OK;
+  if (!q || !k || !v || !k_pool || !v_pool || !q_out || !rope->d_positions || !rope->d_inv_freq) return PA_ERR_INVALID;
+  const void* ptrs[] = {q, k, v, k_pool, v_pool, q_out};
+  for (const void* p : ptrs)
+    if (!pa_aligned16(p)) return PA_ERR_INVALID;
+  const int64_t hq = (int64_t)b->num_q_heads * b->head_dim, hk = (int64_t)b->num_kv_heads * b->head_dim;
+  if (q_row_stride < hq || k_row_stride < hk || v_row_stride < hk || (q_row_stride | k_row_stride | v_row_stride) % 8)
+    return PA_ERR_INVALID;
+  pa::RopeArgs a{};
+  a.b = pa_device_sessions(*b);
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.q_stride = q_row_stride;
+  a.k_stride = k_row_stride;
+  a.v_stride = v_row_stride;
+  a.positions = rope->d_positions;
+  a.inv_freq = rope->d_inv_freq;
+  a.k_pool = static_cast<uint16_t*>(k_pool);
+  a.v_pool = static_cast<uint16_t*>(v_pool);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.R = rope->rotary_dim;
+  a.interleaved = rope->interleaved;
+  if (rope->axes)
+    for (int i = 0; i < rope->rotary_dim / 2; ++i) a.axes[i >> 4] |= (uint32_t)rope->axes[i] << (2 * (i & 15));
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (b->head_dim == 64) pa::rope_append_kernel<64, 1><<<b->num_rows, pa::kRopeThreads, 0, cs>>>(a);
+  else pa::rope_append_kernel<128, 1><<<b->num_rows, pa::kRopeThreads, 0, cs>>>(a);
+  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}

@@ -1,0 +1,86 @@
+// What the session-cache operators share: the batch of sessions as the device
+// sees it, the lookup of a row's session, and the rule of visibility.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "pa.h"
+
+namespace pa {
+
+constexpr int kPage = 16;  // tokens of a page
+
+// A pa_sessions by value, with the pools' head layout.  Every index read from
+// the device arrays is clamped or range-checked where it is read, so that no
+// content of theirs leads out of a buffer.
+struct Sessions {
+  int S, rows, Hq, Hkv, max_pages, num_pages;
+  const int32_t* table;
+  const int32_t* kv_lens;
+  const int32_t* cu_rows;
+
+  __device__ __forceinline__ int kv_len(int s) const { return min(max(kv_lens[s], 0), max_pages * kPage); }
+  __device__ __forceinline__ int row_begin(int s) const { return min(max(cu_rows[s], 0), rows); }
+  // The page of logical page j of session s; -1: a hole (an id outside the pool)
+  __device__ __forceinline__ int page(int s, int j) const {
+    const int p = table[(size_t)s * max_pages + j];
+    return (unsigned)p < (unsigned)num_pages ? p : -1;
+  }
+};
+
+// A row at cached position p sees token t of its session.
+struct Window {
+  int window, sinks;  // window 0: no limit
+  __device__ __forceinline__ bool sees(int p, int t) const {
+    return t <= p && (window == 0 || t > p - window || t < sinks);
+  }
+  // first token past the sinks that a row at position p sees (0 without a window)
+  __device__ __forceinline__ int first(int p) const { return window == 0 ? 0 : max(0, p - window + 1); }
+};
+
+// The session whose rows contain row r (a whole warp asks; every lane gets the
+// answer): the last s with cu_rows[s] <= r.  A 32-way search, so one round
+// trip for up to 32 sessions and two for up to 1024.
+__device__ __forceinline__ int warp_find_session(const Sessions& b, int r, int lane) {
+  int lo = 0, n = b.S;  // cu_rows[lo] <= r, the answer in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) >> 5;
+    const int j = lo + lane * step;
+    const bool le = lane == 0 || (j < lo + n && b.cu_rows[j] <= r);
+    const unsigned m = __ballot_sync(0xffffffffu, le);
+    const int k = 31 - __clz(m);
+    n = min(step, n - k * step);
+    lo += k * step;
+  }
+  return lo;
+}
+
+}  // namespace pa
+
+// Host side: checks of a pa_sessions that every operator makes.  `rows`: the
+// operator uses the rows of the batch (cu_rows).
+inline pa_status pa_check_sessions(const pa_sessions* b, bool rows) {
+  if (!b || b->n_sessions < 1 || b->max_pages < 1 || b->num_pages_in_pool < 1 || b->num_q_heads < 1 ||
+      b->num_kv_heads < 1 || !b->d_block_table || !b->d_kv_lens)
+    return PA_ERR_INVALID;
+  if (b->num_q_heads % b->num_kv_heads || b->n_sessions > 65535 || b->num_kv_heads > 65535) return PA_ERR_INVALID;
+  if ((int64_t)b->n_sessions * b->num_kv_heads > INT32_MAX / 2) return PA_ERR_UNSUPPORTED;
+  if (rows && (b->num_rows < 0 || !b->d_cu_rows)) return PA_ERR_INVALID;
+  if (b->page_size != pa::kPage || !(b->head_dim == 64 || b->head_dim == 128)) return PA_ERR_UNSUPPORTED;
+  const int G = b->num_q_heads / b->num_kv_heads;
+  if (!(G == 1 || G == 2 || G == 4 || G == 8)) return PA_ERR_UNSUPPORTED;
+  // token indices and pool rows are 32-bit
+  if ((int64_t)b->max_pages * pa::kPage > INT32_MAX / 2) return PA_ERR_UNSUPPORTED;
+  if ((int64_t)b->num_pages_in_pool * b->num_kv_heads * pa::kPage > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  return PA_OK;
+}
+
+inline pa::Sessions pa_device_sessions(const pa_sessions& b) {
+  return pa::Sessions{b.n_sessions, b.num_rows,      b.num_q_heads, b.num_kv_heads, b.max_pages, b.num_pages_in_pool,
+                      b.d_block_table, b.d_kv_lens, b.d_cu_rows};
+}
+
+inline bool pa_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }

@@ -10,8 +10,9 @@ builds the decode batch of every registered query for the planner
 (pa_plan_create, or pa_plan_advance between steps, since a session only grows).
 
 It moves no data: appends and forks return the page slots the caller writes
-new K/V into, and the page copies a fork needs; the device pools stay the
-caller's.  Shared pages are reference-counted and go back to the free list
+new K/V into (rope_append writes them from `tables`), and the page copies a fork
+needs; `compact` gives the pages that an eviction copies the kept tokens to.
+The device pools stay the caller's.  Shared pages are reference-counted and go back to the free list
 when no session holds them.
 """
 from __future__ import annotations
@@ -110,6 +111,26 @@ class SessionPool:
             left -= take
         return runs
 
+    def compact(self, sid: int, max_tokens: int) -> List[int]:
+        """Cuts session `sid` to at most max_tokens tokens, on pages of its own:
+        the bookkeeping of an eviction (evict_tokens), which copies the kept
+        tokens to the pages returned here, from those that `tables` gave before.
+        The old pages are released (a fork keeps the ones it shares), so what
+        next takes them must be ordered after that copy.  A pool without enough
+        free pages raises MemoryError and changes nothing."""
+        if max_tokens < 1:
+            raise ValueError("max_tokens must be positive")
+        s = self._sessions[sid]
+        n = min(s.n_tokens, int(max_tokens))
+        need = -(-n // self.P)
+        if need > len(self._free):
+            raise MemoryError("KV pool has no free page")
+        new = [self._take() for _ in range(need)]
+        for p in s.pages:
+            self._drop(p)
+        s.pages, s.n_tokens = new, n
+        return list(new)
+
     def close(self, sid: int):
         s = self._sessions.pop(sid)
         for p in s.pages:
@@ -146,6 +167,17 @@ class SessionPool:
             bt[i, :len(s.pages)] = s.pages
             kv[i] = s.n_tokens
         return [q for _, q in rows], [sid for sid, _ in rows], bt, kv
+
+    def tables(self, sessions=None):
+        """One row per session (all of them, by id, by default), as the
+        session-cache operators take them: block_table int32 [S][max_pages] with -1
+        past the pages, and kv_lens int32 [S]."""
+        sids = sorted(self._sessions) if sessions is None else list(sessions)
+        width = max([len(self._sessions[sid].pages) for sid in sids] + [1])
+        bt = np.full((len(sids), width), -1, dtype=np.int32)
+        for i, sid in enumerate(sids):
+            bt[i, :len(self._sessions[sid].pages)] = self._sessions[sid].pages
+        return bt, np.array([self._sessions[sid].n_tokens for sid in sids], dtype=np.int32)
 
     def check(self):
         """Invariants: every held page is referenced once per session holding
