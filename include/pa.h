@@ -380,13 +380,13 @@ pa_status pa_attend_noalloc(const pa_plan *plan, const void *q, const void *k_po
  *                    as they were.  pa_evict_tokens does not read it (NULL).
  * The i-th of the n rows of a session is its cached token kv_len - n + i (its
  * position).  A block-table entry outside [0, num_pages_in_pool) is a hole: its
- * tokens are neither written, seen nor copied.  Cached tokens of a session
- * hold finite K and V; slots at or past kv_len may hold anything.
+ * tokens are neither written, seen nor copied.  The K and V of tokens that some
+ * row sees are finite; other tokens and slots may hold anything, NaN included.
  * The device arrays are read when the kernels run.  Arguments are checked
  * before anything is enqueued: PA_ERR_INVALID for a null or misaligned pointer
  * (q, k, v, pools, outputs: 16 bytes) or a bad size, PA_ERR_UNSUPPORTED for a
- * head layout, head_dim or page size that is not built or a pool beyond 2^31 - 1
- * (page, head, slot) rows, PA_ERR_CUDA when a launch fails.  All are asynchronous on
+ * head layout, head_dim or page size that is not built, a pool beyond 2^31 - 1
+ * (page, head, slot) rows, or more than 98304 tiles (num_rows / (256 / G) + S), PA_ERR_CUDA when a launch fails.  All are asynchronous on
  * `stream` of the current device, keep nothing between calls and are bit
  * reproducible.
  */
@@ -444,7 +444,7 @@ pa_status pa_window_workspace_size(const pa_sessions *b, int32_t window, int32_t
  * and sinks.  The row at position p sees token t when t <= p and
  * (window == 0 or t > p - window or t < sinks).
  *   window, sinks     >= 0; window 0: no limit
- *   softmax_scale     0 selects 1 / sqrt(D)
+ *   softmax_scale     > 0, finite; 0 selects 1 / sqrt(D)
  *   q                 device bf16 [num_rows][Hq][D]
  *   out               device bf16 [num_rows][Hq][D]
  *   lse               device fp32 [num_rows][Hq], natural log; may be NULL
@@ -454,6 +454,11 @@ pa_status pa_window_workspace_size(const pa_sessions *b, int32_t window, int32_t
 pa_status pa_window_attend(const pa_sessions *b, int32_t window, int32_t sinks, float softmax_scale, const void *q,
                            const void *k_pool, const void *v_pool, void *d_workspace, size_t workspace_bytes,
                            void *out, float *lse, void *stream);
+
+/* The device status word that the last pa_window_attend on this workspace left:
+ * PA_OK, or PA_ERR_TIMEOUT when a device-side bounded wait gave up (its results
+ * are then not to be used).  Synchronises `stream`. */
+pa_status pa_window_status(const void *d_workspace, void *stream, pa_status *out);
 
 /*
  * Weigh: adds to scores the attention weight that every cached token draws from the

@@ -178,6 +178,16 @@ def _workspace(b: PaSessions, window: int, sinks: int, device):
     return torch.empty(n.value, dtype=torch.uint8, device=device)
 
 
+def window_status(workspace, stream=None) -> int:
+    """The device status word of the last window_attend on this workspace
+    (pa_window_status; PA_OK unless a bounded wait gave up).  Synchronises the stream."""
+    out = ctypes.c_int()
+    wp = _ptr(workspace, "workspace", torch.uint8, workspace.device, 256)
+    with _Call(workspace.device, stream) as cs:
+        _check(lib().pa_window_status(wp, cs, ctypes.byref(out)), "pa_window_status")
+    return out.value
+
+
 def window_attend(q, k_pool, v_pool, block_table, kv_lens, cu_rows, *, window: int = 0, sinks: int = 0,
                   softmax_scale: float = 0.0, out=None, lse=None, workspace=None, stream=None):
     """Causal attention of the last rows of every session over its cache, with a

@@ -1,76 +1,774 @@
 // Attention of the last rows of every session over its paged cache: causal,
-// with a sliding window and sinks (pa_window_attend).
+// with a sliding window and sinks (pa_window_attend), on the 5th-generation
+// tensor cores.
 //
 // A row at cached position p sees token t when t <= p and (t > p - window or
 // t < sinks); out = sum_t e^{s_t - m} v_t / l, lse = m + ln l in one pass over
-// the visible tokens with a running maximum.
+// the visible tokens with a running maximum m and sum l.
+//
+// Tiles.  The rows of one kv head are (token, head of the group) pairs, 128 to
+// a tensor-core tile.  A work item is (session, up to 256 / G tokens, kv head)
+// over the pages that any of its rows sees, 8 pages (128 keys) a block:
+//   pair   more than 128 rows: two tiles share every K, V block
+//   alone  at most 128 rows: one tile; even blocks go to one accumulator and
+//          softmax group, odd blocks to the other, joined at the item's end
+// so in both forms two softmax groups alternate and the tensor cores always
+// have a product to run while a group works on its scores.
+//
+// Schedule.  All items' blocks form one line, cut into equal spans, one per CTA
+// (one CTA per SM): every SM gets the same work whatever the lengths.  Lengths
+// live on the device, so every CTA sums the items' blocks itself to find its
+// span.  An item cut by a span's end leaves normalised partial rows (o, lse) in
+// the workspace, at most two a CTA, joined by a short second launch.
+//
+// Roles (384 threads): warps 0-3 and 4-7 softmax groups, one thread per row;
+// warp 8 issues the products; warp 9 walks the items and loads (TMA).  Per
+// block and tile: S = Q K^T (TMEM), P = exp2(S c - m c) rounded to bf16 (half a
+// step, 2^-8 of a weight, averaged over the keys; l sums the unrounded weights)
+// written over S, O += P V (TMEM).  The running maximum is raised, and O
+// rescaled, only when it grows by more than 2^8: numerator and denominator use
+// the same maximum, so the result is unchanged.
 #include "ptx.cuh"
 #include "sessions.cuh"
+#include "tmap.h"
 
 namespace pa {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kThreads = 384;
+constexpr int kMaxChunks = 256;      // chunks of kThreads tile slots that a CTA sums
+constexpr int kQueue = 2;            // entries of the CTA's item queue
+constexpr float kRaise = 8.f;        // log2 growth of a maximum that raises it
+constexpr uint64_t kTimeoutNs = 2000000000ull;
+
+struct Desc {  // a partial item at the head of a CTA's span
+  int first, last;  // CTAs that share the item
+  int slot0;        // partial slot of the first
+  int row0, n_tok, g, pad0, pad1;
+};
 
 struct AttendArgs {
   Sessions b;
   Window w;
-  const uint16_t *q, *k_pool, *v_pool;
+  int lg;              // log2 G
+  int slots, min_span;
+  float scale_log2;
   uint16_t* out;
   float* lse;
-  float scale_log2;
+  int32_t* status;
+  Desc* desc;
+  float *part_lse, *part_o;  // [2 grid][256], [2 grid][256][D]
 };
 
-// One warp per (row, query head); lane l holds dims [l D/32, (l + 1) D/32).
+// What an item's tile slot covers: tokens [i0, i0 + n_tok) of session s, and
+// the virtual pages that its rows see: pages 0 .. ns - 1 (sinks), then from
+// page ns + off on, np in all.
+struct Tile {
+  int s, r0, i0, n_tok, p0;  // r0: first row of the tile; p0: its position
+  int np, ns, off;
+  __device__ __forceinline__ int blocks() const { return (np + 7) >> 3; }
+  __device__ __forceinline__ int page_index(int v) const { return v < ns ? v : v + off; }
+};
+
+// Tile slots: session s owns [cu[s] / T + s, cu[s + 1] / T + s + 1), at least
+// as many as it has tiles of T tokens; the rest are empty.
+__device__ __forceinline__ int slot_begin(const Sessions& b, int s, int lt) { return (b.row_begin(s) >> lt) + s; }
+
+__device__ __forceinline__ Tile make_tile(const AttendArgs& a, int slot, int s) {
+  const int lt = 8 - a.lg;
+  Tile t;
+  t.s = s;
+  const int b0 = a.b.row_begin(s), n = a.b.row_begin(s + 1) - b0, kv = a.b.kv_len(s);
+  t.i0 = (slot - slot_begin(a.b, s, lt)) << lt;
+  t.n_tok = min(1 << lt, n - t.i0);
+  t.r0 = b0 + t.i0;
+  t.p0 = kv - n + t.i0;
+  t.np = t.ns = t.off = 0;
+  if (t.n_tok <= 0 || t.i0 < 0) {
+    t.n_tok = 0;
+    return t;
+  }
+  const int p1 = max(t.p0 + t.n_tok - 1, 0);  // last position; rows that all see nothing get page 0, masked
+  const int last = p1 / kPage, first = a.w.first(max(t.p0, 0)) / kPage;
+  const int sink = (min(a.w.sinks, p1 + 1) + kPage - 1) / kPage;
+  if (sink < first) {
+    t.ns = sink;
+    t.off = first - sink;
+  }
+  t.np = last + 1 - t.off;
+  return t;
+}
+
+// Session of a slot by bisection (one thread).
+__device__ __forceinline__ int find_slot_session(const Sessions& b, int slot, int lt) {
+  int lo = 0, hi = b.S;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (slot_begin(b, mid, lt) <= slot) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// An entry of the item queue: a segment [b0, b1) of an item's blocks.
+struct Item {
+  Tile t;
+  int g, b0, b1;
+  int part;  // partial slot, -1: the whole item
+};
+
 template <int D>
-__global__ void __launch_bounds__(256) window_attend_kernel(const AttendArgs a) {
-  constexpr int W = D / 64;  // bf16x2 words per lane
-  const int lane = threadIdx.x & 31;
-  const int64_t unit = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int r = (int)(unit / a.b.Hq), h = (int)(unit % a.b.Hq);
-  if (r >= a.b.rows) return;
-  const int s = warp_find_session(a.b, r, lane);
-  const int r0 = a.b.row_begin(s), n = a.b.row_begin(s + 1) - r0;
-  if (r < r0 || r >= r0 + n) return;
-  const int p = a.b.kv_len(s) - n + (r - r0), g = h / (a.b.Hq / a.b.Hkv);
-  const uint32_t* q = reinterpret_cast<const uint32_t*>(a.q + ((size_t)r * a.b.Hq + h) * D) + lane * W;
-  float2 qf[W], acc[W];
-#pragma unroll
-  for (int i = 0; i < W; ++i) qf[i] = bf16x2_to_f2(q[i]), acc[i] = make_float2(0.f, 0.f);
-  float m = -INFINITY, l = 0.f;
-  const int first = a.w.first(p);
-  for (int t = min(a.w.sinks, first) > 0 ? 0 : first; t <= p; ++t) {
-    if (t >= a.w.sinks && t < first) t = first;
-    const int page = a.b.page(s, t / kPage);
-    if (page < 0) continue;
-    const size_t at = (((size_t)page * a.b.Hkv + g) * kPage + t % kPage) * D;
-    const uint32_t* k = reinterpret_cast<const uint32_t*>(a.k_pool + at) + lane * W;
-    const uint32_t* v = reinterpret_cast<const uint32_t*>(a.v_pool + at) + lane * W;
-    float x = 0.f;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const float2 kf = bf16x2_to_f2(k[i]);
-      x += qf[i].x * kf.x + qf[i].y * kf.y;
+struct Shape {
+  static constexpr int HALVES = D / 64;
+  static constexpr int BLK = 128 * 128;               // 128 rows x 64 dims
+  static constexpr int TILE = HALVES * BLK;           // a Q tile, a K block, a V block
+  static constexpr int NS = D == 128 ? 5 : 8;         // ring slots
+  static constexpr int OFF_Q = 0, OFF_RING = 2 * TILE, OFF_MISC = OFF_RING + NS * TILE;
+  static constexpr int MISC = 3072;
+  static constexpr int SMEM = OFF_MISC + MISC;
+  static constexpr uint32_t T_S = 0, T_O = 256;       // TMEM columns: S0, S1, O0, O1
+};
+static_assert(Shape<128>::SMEM <= 232448 && Shape<64>::SMEM <= 232448, "shared memory");
+
+struct Misc {
+  uint64_t full[8], empty[8];          // ring
+  uint64_t q_full, q_empty, o_free, joined, done;
+  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t it_full[kQueue], it_empty[kQueue];
+  uint32_t tmem;
+  int fail;
+  Item items[kQueue];
+  float2 exch[2][128];                 // (m, l) of the two groups
+};
+static_assert(sizeof(Misc) <= 3072, "shared memory");
+
+// sums of kThreads slots' blocks, per chunk (aliases the ring before any load)
+struct Sums {
+  long long chunk[kMaxChunks];
+  long long warp[kThreads / 32];
+  long long lo_rest;
+  int lo_slot, pad;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    window_attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap tq,
+                         const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
+  using S = Shape<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (smem_u32(smem) & 1023) {  // the swizzle needs it; the kernel has no other shared memory before it
+    if (threadIdx.x == 0) {
+      a.desc[blockIdx.x].first = -1;
+      record_status(a.status, PA_ERR_DEVICE, blockIdx.x, 0);
     }
+    return;
+  }
+  Misc& mi = *reinterpret_cast<Misc*>(smem + S::OFF_MISC);
+  Sums& su = *reinterpret_cast<Sums*>(smem + S::OFF_RING);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int lt = 8 - a.lg;
+  auto bar = [](uint64_t& b) { return smem_u32(&b); };
+
+  // ---------------- the line of blocks and this CTA's span
+  long long total = 0;
+  const int n_chunks = (a.slots + kThreads - 1) / kThreads;
+  auto slot_blocks = [&](int slot) -> long long {
+    if (slot >= a.slots) return 0;
+    const Tile t = make_tile(a, slot, find_slot_session(a.b, slot, lt));
+    return (long long)t.blocks() * a.b.Hkv;
+  };
+  for (int c = 0; c < n_chunks; ++c) {
+    long long x = slot_blocks(c * kThreads + tid);
 #pragma unroll
     for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    x *= a.scale_log2;
-    const float mn = fmaxf(m, x);
-    const float c = mn == -INFINITY ? 1.f : ex2(m - mn), e = mn == -INFINITY ? 0.f : ex2(x - mn);
-    m = mn;
-    l = l * c + e;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const float2 vf = bf16x2_to_f2(v[i]);
-      acc[i] = make_float2(acc[i].x * c + e * vf.x, acc[i].y * c + e * vf.y);
+    if (lane == 0) su.warp[warp] = x;
+    __syncthreads();
+    if (tid == 0) {
+      long long y = 0;
+      for (int w = 0; w < kThreads / 32; ++w) y += su.warp[w];
+      su.chunk[c] = y;
     }
+    __syncthreads();
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  uint32_t* o = reinterpret_cast<uint32_t*>(a.out + ((size_t)r * a.b.Hq + h) * D) + lane * W;
+  for (int c = 0; c < n_chunks; ++c) total += su.chunk[c];
+  const long long span = max((long long)a.min_span, (total + gridDim.x - 1) / gridDim.x);
+  const long long lo = blockIdx.x * span, hi = min(total, lo + span);
+  if (lo >= total) {
+    if (tid == 0) a.desc[blockIdx.x].first = -1;
+    if (tid == 0 && blockIdx.x == 0) *a.status = 0;
+    return;  // uniform over the CTA
+  }
+  {
+    long long before = 0;
+    int c = 0;
+    while (before + su.chunk[c] <= lo) before += su.chunk[c++];
+    // exclusive prefix inside the chunk
+    const int slot = c * kThreads + tid;
+    const long long x = slot_blocks(slot);
+    long long inc = x;
 #pragma unroll
-  for (int i = 0; i < W; ++i) o[i] = pack_bf16x2(acc[i].x * inv, acc[i].y * inv);
-  if (a.lse && lane == 0) a.lse[(size_t)r * a.b.Hq + h] = l > 0.f ? (m + lg2(l)) * kLn2 : -INFINITY;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    __syncthreads();
+    if (lane == 31) su.warp[warp] = inc;
+    __syncthreads();
+    long long exc = before + inc - x;
+    for (int w = 0; w < warp; ++w) exc += su.warp[w];
+    if (x > 0 && exc <= lo && lo < exc + x) {
+      su.lo_slot = slot;
+      su.lo_rest = lo - exc;
+    }
+    __syncthreads();
+  }
+  const int lo_slot = su.lo_slot;
+  const long long lo_rest = su.lo_rest;
+
+  if (tid == 0) {
+    for (int i = 0; i < S::NS; ++i) {
+      mbar_init(bar(mi.full[i]), 1);
+      mbar_init(bar(mi.empty[i]), 1);
+    }
+    mbar_init(bar(mi.q_full), 1);
+    mbar_init(bar(mi.q_empty), 1);
+    mbar_init(bar(mi.o_free), 8);
+    mbar_init(bar(mi.joined), 8);
+    mbar_init(bar(mi.done), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(mi.s_full[i]), 1);
+      mbar_init(bar(mi.p_full[i]), 4);
+      mbar_init(bar(mi.o_full[i]), 1);
+    }
+    for (int i = 0; i < kQueue; ++i) {
+      mbar_init(bar(mi.it_full[i]), 1);
+      mbar_init(bar(mi.it_empty[i]), 9);  // product warp, 8 softmax warps
+    }
+    mi.fail = 0;
+    if (blockIdx.x == 0) *a.status = 0;
+    fence_mbar_init();
+  }
+  if (warp == 8) tmem_alloc(smem_u32(&mi.tmem), 512);
+  fence_proxy_async_smem();  // the ring held the sums
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = mi.tmem;
+  volatile int* fail = &mi.fail;
+
+  // Wait for a phase; gives up after kTimeoutNs, or when another role has.
+  auto wait = [&](uint64_t& b, int phase, int code) -> bool {
+    const uint32_t ad = bar(b), par = (uint32_t)phase & 1u;
+    if (mbar_try_wait(ad, par)) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+      if (mbar_try_wait(ad, par)) return true;
+      if (*fail) return false;
+      if (global_timer_ns() - t0 > kTimeoutNs) {
+        *fail = 1;
+        record_status(a.status, PA_ERR_TIMEOUT, blockIdx.x, code);
+        return false;
+      }
+    }
+  };
+  // The same by a whole warp: all lanes succeed or none does.
+  auto wwait = [&](uint64_t& b, int phase, int code) -> bool { return __all_sync(0xffffffffu, wait(b, phase, code)); };
+  // Ring position of the loads of a segment of n blocks whose first load is
+  // number `base`: K0 K1 V0 K2 V1 ... V(n-1), the order in which they are used.
+  auto pos_k = [](int base, int j) { return j == 0 ? base : base + 2 * j - 1; };
+  auto pos_v = [](int base, int j, int n) { return j < n - 1 ? base + 2 * j + 2 : base + 2 * n - 1; };
+  uint8_t* ring = smem + S::OFF_RING;
+
+  // Registers: 384 threads x 168 at launch; a softmax thread holds a row of
+  // scores: 2 x 128 x 208 + 128 x 80 of the 64512
+  if (warp == 9) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    // ---------------- items and loads
+    if (lane == 0) {
+      prefetch_tmap(&tq);
+      prefetch_tmap(&tk);
+      prefetch_tmap(&tv);
+    }
+    int slot = lo_slot;
+    Tile t = make_tile(a, slot, find_slot_session(a.b, slot, lt));
+    int g = (int)(lo_rest / t.blocks()), b0 = (int)(lo_rest % t.blocks());
+    long long left = hi - lo;
+    int base = 0, it = 0, issued = 0, n_q = 0;
+    bool ok = true;
+    const int oob = a.b.num_pages * a.b.Hkv * kPage;  // a row past the pool: zeros
+    if (lane == 0) {
+      Desc d{};
+      d.first = -1;
+      if (b0 > 0) {
+        const long long start = lo - b0, end = start + t.blocks();
+        d.first = (int)(start / span);
+        d.last = (int)((end - 1) / span);
+        d.slot0 = start == d.first * span ? 2 * d.first : 2 * d.first + 1;
+        d.row0 = t.r0;
+        d.n_tok = t.n_tok;
+        d.g = g;
+      }
+      a.desc[blockIdx.x] = d;
+    }
+    while (left > 0 && ok) {
+      const int nb = t.blocks();
+      const int b1 = (int)min((long long)nb, b0 + left);
+      const int n = b1 - b0, e = it % kQueue;
+      if (it >= kQueue && !wwait(mi.it_empty[e], it / kQueue - 1, 1)) break;
+      if (lane == 0) {
+        Item& x = mi.items[e];
+        x.t = t;
+        x.g = g;
+        x.b0 = b0;
+        x.b1 = b1;
+        x.part = b0 == 0 && b1 == nb ? -1 : left == hi - lo ? 2 * (int)blockIdx.x : 2 * (int)blockIdx.x + 1;
+        mbar_arrive(bar(mi.it_full[e]));
+      }
+      if (it > 0 && !wwait(mi.q_empty, it - 1, 2)) break;
+      const bool pair = (t.n_tok << a.lg) > 128;
+      ++n_q;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar(mi.q_full), (pair ? 2 : 1) * S::TILE);
+        for (int i = 0; i < (pair ? 2 : 1); ++i)
+          for (int h = 0; h < S::HALVES; ++h)
+            tma_load_3d(smem_u32(smem + S::OFF_Q + i * S::TILE + h * S::BLK), &tq, 64 * h, g << a.lg,
+                        t.r0 + i * (128 >> a.lg), bar(mi.q_full));
+      }
+      // rows of the pool of the block's pages, lane l < 8: page 8 j + l
+      auto rows_of = [&](int j) -> int {
+        const int v = 8 * j + lane;
+        if (lane >= 8 || v >= t.np) return -1;
+        const int pg = a.b.page(t.s, t.page_index(v));
+        return pg < 0 ? oob : (pg * a.b.Hkv + g) * kPage;
+      };
+      auto load = [&](int pos, const CUtensorMap* tm, int j, int row) -> bool {
+        const int sl = pos % S::NS;
+        if (pos >= S::NS && !wwait(mi.empty[sl], pos / S::NS - 1, 3)) return false;
+        const int np = min(8, t.np - 8 * j);
+        issued = pos + 1;
+        if (lane == 0) mbar_arrive_expect_tx(bar(mi.full[sl]), (uint32_t)np * kPage * D * 2);
+        __syncwarp();
+        if (lane < np) {
+          const uint32_t dst = smem_u32(ring + sl * S::TILE) + lane * 2048;
+#pragma unroll
+          for (int h = 0; h < S::HALVES; ++h) tma_load_2d(dst + h * S::BLK, tm, 64 * h, row, bar(mi.full[sl]));
+        }
+        return true;
+      };
+      int row = rows_of(b0), prev = row;
+      for (int j = 0; j < n && ok; ++j) {
+        const int next = j + 1 < n ? rows_of(b0 + j + 1) : -1;
+        ok = load(pos_k(base, j), &tk, b0 + j, row);
+        if (ok && j > 0) ok = load(pos_v(base, j - 1, n), &tv, b0 + j - 1, prev);
+        prev = row;
+        row = next;
+      }
+      if (ok) ok = load(pos_v(base, n - 1, n), &tv, b1 - 1, prev);
+      base += 2 * n;
+      left -= n;
+      ++it;
+      b0 = 0;
+      if (++g == a.b.Hkv) {
+        g = 0;
+        while (left > 0 && ++slot < a.slots) {
+          t = make_tile(a, slot, find_slot_session(a.b, slot, lt));
+          if (t.np > 0) break;
+        }
+      }
+    }
+    // end of the line for the other roles
+    const int e = it % kQueue;
+    if (it < kQueue || wwait(mi.it_empty[e], it / kQueue - 1, 4)) {
+      if (lane == 0) {
+        mi.items[e].b1 = -1;
+        mbar_arrive(bar(mi.it_full[e]));
+      }
+    }
+    // loads in flight land before the CTA ends (all of them have, unless a wait gave up)
+    for (int p = max(0, issued - S::NS); p < issued; ++p)
+      mbar_wait_bounded(bar(mi.full[p % S::NS]), (p / S::NS) & 1, kTimeoutNs);
+    if (n_q > 0) mbar_wait_bounded(bar(mi.q_full), (n_q - 1) & 1, kTimeoutNs);
+  } else if (warp == 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    // ---------------- products
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = umma_idesc_bf16(128, 128, false, false);
+      constexpr uint32_t idesc_o = umma_idesc_bf16(128, D, false, true);
+      int base = 0, it = 0, cs[2] = {0, 0};  // cs: P phases used by each tile
+      bool ok = true;
+      while (ok) {
+        const int e = it % kQueue;
+        if (!wait(mi.it_full[e], it / kQueue, 5)) break;
+        const Item& x = mi.items[e];
+        const int n = x.b1 - x.b0, np = x.t.np, jb = x.b0;
+        const bool end = x.b1 < 0, pair = (x.t.n_tok << a.lg) > 128;
+        mbar_arrive(bar(mi.it_empty[e]));
+        if (end) break;
+        auto issue_s = [&](int tile, int q, int pos) {
+          const uint32_t qa = smem_u32(smem + S::OFF_Q + q * S::TILE), ka = smem_u32(ring + (pos % S::NS) * S::TILE);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint64_t ad = umma_sdesc_sw128(qa + (k >> 2) * S::BLK + (k & 3) * 32, 1, 64);
+            const uint64_t bd = umma_sdesc_sw128(ka + (k >> 2) * S::BLK + (k & 3) * 32, 1, 64);
+            umma_bf16(tmem + S::T_S + tile * 128, ad, bd, idesc_s, k > 0 ? 1u : 0u);
+          }
+          umma_commit(bar(mi.s_full[tile]));
+        };
+        auto issue_o = [&](int tile, int j, int pos, bool first) {
+          const uint32_t va = smem_u32(ring + (pos % S::NS) * S::TILE);
+          const int pages = min(8, np - 8 * (jb + j));
+          for (int c = 0; c < pages; ++c)
+            umma_bf16_ts(tmem + S::T_O + tile * D, tmem + S::T_S + tile * 128 + 8 * c,
+                         umma_sdesc_sw128(va + c * 2048, S::BLK >> 4, 64), idesc_o, first && c == 0 ? 0u : 1u);
+        };
+        auto wait_load = [&](int pos) -> bool { return wait(mi.full[pos % S::NS], pos / S::NS, 6); };
+        if (!wait(mi.q_full, it, 7)) break;
+        if (pair) {
+          ok = wait_load(pos_k(base, 0));
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(0, 0, pos_k(base, 0));
+          issue_s(1, 1, pos_k(base, 0));
+          umma_commit(bar(mi.empty[pos_k(base, 0) % S::NS]));
+          if (n == 1) umma_commit(bar(mi.q_empty));
+          for (int j = 0; j < n && ok; ++j) {
+            const int pv = pos_v(base, j, n), pk = pos_k(base, j + 1);
+            for (int tile = 0; tile < 2 && ok; ++tile) {
+              ok = wait(mi.p_full[tile], cs[tile]++, 8) && (tile || wait_load(pv)) &&
+                   (tile || j || it == 0 || wait(mi.o_free, it - 1, 9));
+              if (!ok) break;
+              tc_fence_after();
+              issue_o(tile, j, pv, j == 0);
+              if (j == n - 1) umma_commit(bar(mi.o_full[tile]));
+              if (tile == 1) umma_commit(bar(mi.empty[pv % S::NS]));
+              if (j + 1 < n) {
+                if (!tile && !(ok = wait_load(pk))) break;
+                tc_fence_after();
+                issue_s(tile, tile, pk);
+                if (tile == 1) {
+                  umma_commit(bar(mi.empty[pk % S::NS]));
+                  if (j + 2 == n) umma_commit(bar(mi.q_empty));
+                }
+              }
+            }
+          }
+        } else {
+          for (int j = 0; j < min(n, 2) && ok; ++j) {
+            const int pk = pos_k(base, j);
+            if (!(ok = wait_load(pk))) break;
+            tc_fence_after();
+            issue_s(j, 0, pk);
+            umma_commit(bar(mi.empty[pk % S::NS]));
+            if (j == n - 1) umma_commit(bar(mi.q_empty));
+          }
+          for (int j = 0; j < n && ok; ++j) {
+            const int tile = j & 1, pv = pos_v(base, j, n);
+            ok = wait(mi.p_full[tile], cs[tile]++, 10) && wait_load(pv) && (j || it == 0 || wait(mi.o_free, it - 1, 11));
+            if (!ok) break;
+            tc_fence_after();
+            issue_o(tile, j, pv, j < 2);
+            umma_commit(bar(mi.empty[pv % S::NS]));
+            if (j + 2 >= n) umma_commit(bar(mi.o_full[tile]));
+            if (j + 2 < n) {
+              const int pk = pos_k(base, j + 2);
+              if (!(ok = wait_load(pk))) break;
+              tc_fence_after();
+              issue_s(tile, 0, pk);
+              umma_commit(bar(mi.empty[pk % S::NS]));
+              if (j + 3 == n) umma_commit(bar(mi.q_empty));
+            }
+          }
+        }
+        base += 2 * n;
+        ++it;
+      }
+      // every product issued has completed before the tensor memory is released
+      umma_commit(bar(mi.done));
+      mbar_wait_bounded(bar(mi.done), 0, kTimeoutNs);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ---------------- softmax: group `grp`, row (= TMEM lane) quad * 32 + lane of its tile
+    const int grp = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
+    const uint32_t t_s = tmem + S::T_S + grp * 128 + lane_off, t_o = tmem + S::T_O + grp * D + lane_off;
+    int it = 0, base = 0, ps = 0, po = 0, pj = 0;  // phases used of s_full, o_full, joined
+    bool ok = true;
+    while (ok) {
+      const int e = it % kQueue;
+      if (!wwait(mi.it_full[e], it / kQueue, 12)) break;
+      const Tile t = mi.items[e].t;
+      const int g = mi.items[e].g, b0 = mi.items[e].b0, b1 = mi.items[e].b1, part = mi.items[e].part;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(mi.it_empty[e]));
+      if (b1 < 0) break;
+      const int n = b1 - b0;
+      const bool pair = (t.n_tok << a.lg) > 128;
+      const int tok0 = pair ? grp << (7 - a.lg) : 0;     // first token of this group's tile
+      const int tok = tok0 + (row >> a.lg);              // this row's token
+      const int p = t.p0 + min(tok, t.n_tok - 1);        // rows past the tile repeat its last
+      const int p_min = t.p0 + tok0, p_max = t.p0 + min(tok0 + (128 >> a.lg), t.n_tok) - 1;
+      const int kv_end = a.b.kv_len(t.s), seen_from = a.w.first(max(t.p0, 0));
+      // the page (or hole, -1) of lane's page of block j, asked for a block ahead
+      auto page_of = [&](int j) -> int {
+        const int v = 8 * (b0 + j) + lane;
+        return j < n && lane < 8 && v < t.np ? a.b.page(t.s, t.page_index(v)) : 0;
+      };
+      int page_next = page_of(pair ? 0 : grp);
+      float m = -INFINITY, l = 0.f;
+      bool first = true;
+      for (int j = pair ? 0 : grp; j < n && ok; j += pair ? 1 : 2) {
+        const int v0 = 8 * (b0 + j), pages = min(8, t.np - v0);
+        const unsigned holes = __ballot_sync(0xffffffffu, page_next < 0);
+        page_next = page_of(j + (pair ? 1 : 2));
+        const int t_first = t.page_index(v0) * kPage, t_last = t.page_index(v0 + pages - 1) * kPage + kPage - 1;
+        const bool all = pages == 8 && holes == 0 && t_last <= p_min &&
+                         (a.w.window == 0 || (v0 >= t.ns && t_first > p_max - a.w.window) || t_last < a.w.sinks);
+        if (!(ok = wwait(mi.s_full[grp], ps++, 13))) break;
+        tc_fence_after();
+        float x[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, x[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_wait_ld_into(x[c]);
+        if (!all) {
+#pragma unroll
+          for (int pg = 0; pg < 8; ++pg) {
+            const int t0 = t.page_index(v0 + pg) * kPage;
+            const bool gone = pg >= pages || (holes >> pg & 1);
+            const int top = gone ? -1 : p - t0;                                   // x <= top
+            const int low = a.w.window ? p - a.w.window - t0 : INT32_MIN, sk = a.w.sinks - t0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (!(i <= top && (i > low || i < sk))) x[pg >> 1][16 * (pg & 1) + i] = -INFINITY;
+          }
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 128; i += 2) mx = fmaxf(mx, fmaxf(x[i >> 5][i & 31], x[i >> 5][(i & 31) + 1]));
+        mx *= a.scale_log2;
+        if (first) {
+          m = mx;
+        } else if (__any_sync(0xffffffffu, mx > m + kRaise)) {
+          const float mn = mx > m + kRaise ? mx : m;
+          const float f = mn == -INFINITY ? 1.f : ex2(m - mn);  // O and l are 0 while m is -inf
+          l *= f;
+          m = mn;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            float o[32];
+            tmem_ld32(t_o + c, o);
+            tmem_wait_ld_into(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= f;
+            tmem_st32(t_o + c, o);
+          }
+          tmem_wait_st();
+        }
+        first = false;
+        const float mc = m == -INFINITY ? 0.f : -m;
+        const float2 sc = make_float2(a.scale_log2, a.scale_log2), mm = make_float2(mc, mc);
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float pw[32];  // 16 words of two weights
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float2 y = ffma2(make_float2(x[c][i], x[c][i + 1]), sc, mm);
+            const float e0 = ex2(y.x), e1 = ex2(y.y);
+            sum = ffma2(make_float2(e0, e1), make_float2(1.f, 1.f), sum);
+            pw[i >> 1] = __uint_as_float(pack_bf16x2(e0, e1));
+          }
+          tmem_st16<0>(t_s + 16 * c, pw);
+        }
+        l += sum.x + sum.y;
+        // tokens that no row of the item sees (past the session's end, between the
+        // sinks and the first window) may hold anything: a weight of 0 times NaN is
+        // NaN, so their V rows are zeroed; the first tile of a pair does it for both
+        bool dead = false;
+        if (lane < pages) {
+          const int t0 = t.page_index(v0 + lane) * kPage;
+          dead = t0 + kPage > kv_end || (t0 + kPage > a.w.sinks && t0 < seen_from);
+        }
+        if (__any_sync(0xffffffffu, dead) && (grp == 0 || !pair)) {
+          const int pv = pos_v(base, j, n);
+          if (!(ok = wwait(mi.full[pv % S::NS], pv / S::NS, 14))) break;
+          const int key = tid & 127, tk0 = t.page_index(v0 + (key >> 4)) * kPage + (key & 15);
+          if ((key >> 4) < pages && (tk0 >= kv_end || (tk0 >= a.w.sinks && tk0 < seen_from))) {
+            uint8_t* vt = ring + (pv % S::NS) * S::TILE + key * 128;
+#pragma unroll
+            for (int i = 0; i < 8 * S::HALVES; ++i)
+              *reinterpret_cast<uint4*>(vt + (i >> 3) * S::BLK + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(mi.p_full[grp]));
+      }
+      if (!ok) break;
+      // ---------------- the item's end
+      const int mine = pair ? n : (n - grp + 1) >> 1;  // blocks of this group
+      if (mine > 0 && !(ok = wwait(mi.o_full[grp], po++, 15))) break;
+      tc_fence_after();
+      float w0 = l > 0.f ? 1.f / l : 0.f, w1 = 0.f, lse2 = l > 0.f ? m + lg2(l) : -INFINITY;
+      int d0 = 0, dn = D;  // dims this thread writes
+      uint32_t src0 = t_o, src1 = t_o;
+      bool two = false;
+      if (!pair) {
+        mi.exch[grp][row] = make_float2(m, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(mi.joined));
+        if (!(ok = wwait(mi.joined, pj++, 16))) break;
+        tc_fence_after();
+        const float2 ml = mi.exch[grp ^ 1][row];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(mi.joined));  // read by both before the next item's are written
+        if (!(ok = wwait(mi.joined, pj++, 17))) break;
+        const float mm = fmaxf(m, ml.x);
+        const float f0 = l > 0.f ? ex2(m - mm) : 0.f, f1 = ml.y > 0.f ? ex2(ml.x - mm) : 0.f;
+        const float lt2 = l * f0 + ml.y * f1, inv = lt2 > 0.f ? 1.f / lt2 : 0.f;
+        lse2 = lt2 > 0.f ? mm + lg2(lt2) : -INFINITY;
+        w0 = f0 * inv;
+        w1 = f1 * inv;
+        d0 = grp * (D / 2);
+        dn = D / 2;
+        src1 = tmem + S::T_O + (grp ^ 1) * D + lane_off;
+        two = n > 1;
+      }
+      const bool have = mine > 0;  // this group's accumulator was written
+      const bool live = tok < t.n_tok;
+      const int r = t.r0 + tok, h = (g << a.lg) + (row & ((1 << a.lg) - 1));
+      const int prow = (pair ? grp * 128 : 0) + row;
+#pragma unroll 1
+      for (int c = d0; c < d0 + dn; c += 32) {
+        float o[32];
+        if (have) {
+          tmem_ld32(src0 + c, o);
+          tmem_wait_ld_into(o);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = have ? o[i] * w0 : 0.f;
+        if (two || (!pair && !have)) {
+          float o1[32];
+          tmem_ld32(src1 + c, o1);
+          tmem_wait_ld_into(o1);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] += o1[i] * w1;
+        }
+        if (live) {
+          if (part < 0) {
+            uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + ((size_t)r * a.b.Hq + h) * D + c);
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+              *reinterpret_cast<uint4*>(dst + i / 2) =
+                  make_uint4(pack_bf16x2(o[i], o[i + 1]), pack_bf16x2(o[i + 2], o[i + 3]),
+                             pack_bf16x2(o[i + 4], o[i + 5]), pack_bf16x2(o[i + 6], o[i + 7]));
+          } else {
+            float* dst = a.part_o + ((size_t)part * 256 + prow) * D + c;
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+              st_global_v8(dst + i, o[i], o[i + 1], o[i + 2], o[i + 3], o[i + 4], o[i + 5], o[i + 6], o[i + 7]);
+          }
+        }
+      }
+      if (live && (pair || grp == 0)) {
+        if (part < 0) {
+          if (a.lse) a.lse[(size_t)r * a.b.Hq + h] = lse2 * kLn2;
+        } else {
+          a.part_lse[(size_t)part * 256 + prow] = lse2;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(mi.o_free));
+      base += 2 * n;
+      ++it;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  griddep_launch_dependents();
+  if (warp == 8) tmem_free(tmem, 512);
+}
+
+// Joins the partial rows of the items that the spans cut: block (c, y) takes
+// rows [8 y, 8 y + 8) of the item cut at the start of CTA c's span, when c is
+// the first cut of that item.  One warp per row; parts in the order of their
+// keys.
+template <int D>
+__global__ void __launch_bounds__(256) window_join_kernel(const AttendArgs a) {
+  griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int W = D / 32;
+  const Desc d = a.desc[blockIdx.x + 1];
+  if (d.first != (int)blockIdx.x) return;
+  const int prow = blockIdx.y * 8 + warp;
+  const bool pair = (d.n_tok << a.lg) > 128;
+  const int tok = prow >> a.lg;  // tile 1 starts at row 128, token 128 / G
+  if (tok >= d.n_tok || (!pair && prow >= 128)) return;
+  float mx = -INFINITY;
+  for (int c = d.first; c <= d.last; ++c)
+    mx = fmaxf(mx, a.part_lse[(size_t)(c == d.first ? d.slot0 : 2 * c) * 256 + prow]);
+  float sum = 0.f, acc[W] = {};
+  for (int c = d.first; c <= d.last; ++c) {
+    const size_t at = (size_t)(c == d.first ? d.slot0 : 2 * c) * 256 + prow;
+    const float f = mx == -INFINITY ? 0.f : ex2(a.part_lse[at] - mx);
+    sum += f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) acc[i] += f * a.part_o[at * D + lane * W + i];
+  }
+  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const size_t ro = (size_t)(d.row0 + tok) * a.b.Hq + (d.g << a.lg) + (prow & ((1 << a.lg) - 1));
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + ro * D) + lane * (W / 2);
+#pragma unroll
+  for (int i = 0; i < W; i += 2) dst[i / 2] = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+  if (a.lse && lane == 0) a.lse[ro] = sum > 0.f ? (mx + lg2(sum)) * kLn2 : -INFINITY;
+}
+
+// log2 of G (1, 2, 4, 8)
+int log2_group(const pa_sessions& b) {
+  const int G = b.num_q_heads / b.num_kv_heads;
+  return G == 8 ? 3 : G == 4 ? 2 : G == 2 ? 1 : 0;
+}
+
+struct Launch {
+  int grid, slots, min_span;
+  size_t off_desc, off_lse, off_o, bytes;
+};
+
+// At most one CTA per SM, and no more than the longest possible line of blocks fills.
+bool plan_launch(const pa_sessions& b, const Window& w, Launch* out) {
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess)
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaGetLastError();
+  const int T = 256 >> log2_group(b);
+  const int64_t slots = (int64_t)b.num_rows / T + b.n_sessions;
+  if (slots > (int64_t)kMaxChunks * kThreads) return false;
+  int64_t pages = b.max_pages;
+  if (w.window) {
+    const int64_t seen = ((int64_t)w.window + T + kPage - 2) / kPage + 1 + ((int64_t)w.sinks + kPage - 1) / kPage + 1;
+    if (seen < pages) pages = seen;
+  }
+  const int64_t line = slots * b.num_kv_heads * ((pages + 7) / 8);
+  out->min_span = 2;
+  const int64_t most = (line + out->min_span - 1) / out->min_span;
+  out->grid = (int)(most < sms ? (most < 1 ? 1 : most) : sms);
+  out->slots = (int)slots;
+  out->off_desc = 256;
+  out->off_lse = out->off_desc + ((size_t)out->grid * sizeof(Desc) + 255) / 256 * 256;
+  out->off_o = out->off_lse + (size_t)out->grid * 2 * 256 * 4;
+  out->bytes = out->off_o + (size_t)out->grid * 2 * 256 * b.head_dim * 4;
+  return true;
 }
 
 }  // namespace
@@ -80,35 +778,81 @@ extern "C" pa_status pa_window_workspace_size(const pa_sessions* b, int32_t wind
   const pa_status st = pa_check_sessions(b, true);
   if (st != PA_OK) return st;
   if (!bytes || window < 0 || sinks < 0) return PA_ERR_INVALID;
-  *bytes = 256;
+  pa::Launch l;
+  if (!pa::plan_launch(*b, pa::Window{window, sinks}, &l)) return PA_ERR_UNSUPPORTED;
+  *bytes = l.bytes;
   return PA_OK;
 }
+
+extern "C" pa_status pa_window_status(const void* d_workspace, void* stream, pa_status* out) {
+  if (!d_workspace || !out) return PA_ERR_INVALID;
+  int32_t word = 0;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (cudaMemcpyAsync(&word, d_workspace, 4, cudaMemcpyDeviceToHost, cs) != cudaSuccess) return PA_ERR_CUDA;
+  if (cudaStreamSynchronize(cs) != cudaSuccess) return PA_ERR_CUDA;
+  *out = static_cast<pa_status>(word);
+  return PA_OK;
+}
+
+namespace {
+
+template <int D>
+bool launch(const pa::AttendArgs& a, const pa::Launch& l, const CUtensorMap& tq, const CUtensorMap& tk,
+            const CUtensorMap& tv, cudaStream_t cs) {
+  auto* k = pa::window_attend_kernel<D>;
+  constexpr int smem = pa::Shape<D>::SMEM;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
+  k<<<l.grid, pa::kThreads, smem, cs>>>(a, tq, tk, tv);
+  if (cudaGetLastError() != cudaSuccess) return false;
+  if (l.grid == 1) return true;  // one CTA cuts no item
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(l.grid - 1, 32);
+  cfg.blockDim = dim3(256);
+  cfg.stream = cs;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, pa::window_join_kernel<D>, a) == cudaSuccess;
+}
+
+}  // namespace
 
 extern "C" pa_status pa_window_attend(const pa_sessions* b, int32_t window, int32_t sinks, float softmax_scale,
                                       const void* q, const void* k_pool, const void* v_pool, void* d_workspace,
                                       size_t workspace_bytes, void* out, float* lse, void* stream) {
-  size_t need = 0;
-  const pa_status st = pa_window_workspace_size(b, window, sinks, &need);
+  const pa_status st = pa_check_sessions(b, true);
   if (st != PA_OK) return st;
+  if (window < 0 || sinks < 0 || !(softmax_scale >= 0.f) || softmax_scale > 3.4e38f) return PA_ERR_INVALID;
+  pa::Launch l;
+  if (!pa::plan_launch(*b, pa::Window{window, sinks}, &l)) return PA_ERR_UNSUPPORTED;
   if (b->num_rows == 0) return PA_OK;
   if (!q || !k_pool || !v_pool || !out || !d_workspace) return PA_ERR_INVALID;
   if (!pa_aligned16(q) || !pa_aligned16(k_pool) || !pa_aligned16(v_pool) || !pa_aligned16(out) ||
       (reinterpret_cast<uintptr_t>(d_workspace) & 255))
     return PA_ERR_INVALID;
-  if (workspace_bytes < need) return PA_ERR_NOMEM;
+  if (workspace_bytes < l.bytes) return PA_ERR_NOMEM;
   pa::AttendArgs a{};
   a.b = pa_device_sessions(*b);
   a.w = pa::Window{window, sinks};
-  a.q = static_cast<const uint16_t*>(q);
-  a.k_pool = static_cast<const uint16_t*>(k_pool);
-  a.v_pool = static_cast<const uint16_t*>(v_pool);
+  a.lg = pa::log2_group(*b);
+  a.slots = l.slots;
+  a.min_span = l.min_span;
+  a.scale_log2 = (softmax_scale != 0.f ? softmax_scale : 1.f / sqrtf((float)b->head_dim)) * pa::kLog2e;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
-  a.scale_log2 = (softmax_scale != 0.f ? softmax_scale : 1.f / sqrtf((float)b->head_dim)) * pa::kLog2e;
+  uint8_t* ws = static_cast<uint8_t*>(d_workspace);
+  a.status = reinterpret_cast<int32_t*>(ws);
+  a.desc = reinterpret_cast<pa::Desc*>(ws + l.off_desc);
+  a.part_lse = reinterpret_cast<float*>(ws + l.off_lse);
+  a.part_o = reinterpret_cast<float*>(ws + l.off_o);
+  const int D = b->head_dim, G = 1 << a.lg;
+  CUtensorMap tq, tk, tv;
+  if (!pa::tmap_q(&tq, q, b->num_rows, b->num_q_heads, D, G, 128 / G) ||
+      !pa::tmap_pool(&tk, k_pool, b->num_pages_in_pool, b->num_kv_heads, D) ||
+      !pa::tmap_pool(&tv, v_pool, b->num_pages_in_pool, b->num_kv_heads, D))
+    return PA_ERR_CUDA;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const int64_t units = (int64_t)b->num_rows * b->num_q_heads;
-  const unsigned grid = (unsigned)((units + 7) / 8);
-  if (b->head_dim == 64) pa::window_attend_kernel<64><<<grid, 256, 0, cs>>>(a);
-  else pa::window_attend_kernel<128><<<grid, 256, 0, cs>>>(a);
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  return (D == 64 ? launch<64>(a, l, tq, tk, tv, cs) : launch<128>(a, l, tq, tk, tv, cs)) ? PA_OK : PA_ERR_CUDA;
 }
