@@ -28,6 +28,8 @@
 // written over S, O += P V (TMEM).  The running maximum is raised, and O
 // rescaled, only when it grows by more than 2^8: numerator and denominator use
 // the same maximum, so the result is unchanged.
+#include <type_traits>
+
 #include "ptx.cuh"
 #include "sessions.cuh"
 #include "tmap.h"
@@ -40,6 +42,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kThreads = 384;
 constexpr int kMaxChunks = 256;      // chunks of kThreads tile slots that a CTA sums
 constexpr int kQueue = 2;            // entries of the CTA's item queue
+constexpr int kFmaPairs = 4;           // of the 16 pairs of scores of a 32-key chunk: exponentials on the FMA pipe
 constexpr float kRaise = 8.f;        // log2 growth of a maximum that raises it
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
@@ -135,7 +138,7 @@ static_assert(Shape<128>::SMEM <= 232448 && Shape<64>::SMEM <= 232448, "shared m
 struct Misc {
   uint64_t full[8], empty[8];          // ring
   uint64_t q_full, q_empty, o_free, joined, done;
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2], p_full[2][2], o_full[2];  // p_full: by tile and half of the block's keys
   uint64_t it_full[kQueue], it_empty[kQueue];
   uint32_t tmem;
   int fail;
@@ -151,6 +154,51 @@ struct Sums {
   long long lo_rest;
   int lo_slot, pad;
 };
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
+// umma_sdesc_sw128 from an address already in 16-byte units.
+__device__ __forceinline__ uint64_t sdesc_sw128_lo(uint32_t addr16, uint32_t lbo16, uint32_t sbo16) {
+  return (uint64_t)(addr16 | (lbo16 << 16)) | ((uint64_t)(sbo16 | (1u << 14) | (2u << 29)) << 32);
+}
+
+// 2^x of two finite x <= 127 on the FMA pipe: x = n + f, f in [-1/2, 1/2]; 2^f by
+// the degree-5 polynomial of least relative error (Remez exchange, 7.5e-8), n
+// added to the exponent.  x below -126 counts as -126.
+__device__ __forceinline__ float2 exp2_fma(float2 x) {
+  x.x = fmaxf(x.x, -126.f);
+  x.y = fmaxf(x.y, -126.f);
+  const float2 big = make_float2(12582912.f, 12582912.f);  // 1.5 * 2^23: adding it rounds to an integer
+  const float2 t = fadd2(x, big);
+  const float2 f = fadd2(x, fmul2(fadd2(t, make_float2(-12582912.f, -12582912.f)), make_float2(-1.f, -1.f)));
+  float2 p = make_float2(1.3276472454890609e-3f, 1.3276472454890609e-3f);
+  p = ffma2(p, f, make_float2(9.675540961325169e-3f, 9.675540961325169e-3f));
+  p = ffma2(p, f, make_float2(5.550713092088699e-2f, 5.550713092088699e-2f));
+  p = ffma2(p, f, make_float2(0.24022120237350464f, 0.24022120237350464f));
+  p = ffma2(p, f, make_float2(0.6931469440460205f, 0.6931469440460205f));
+  p = ffma2(p, f, make_float2(1.0000001192092896f, 1.0000001192092896f));
+  p.x = __uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23));
+  p.y = __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23));
+  return p;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -239,7 +287,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(mi.done), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(mi.s_full[i]), 1);
-      mbar_init(bar(mi.p_full[i]), 4);
+      mbar_init(bar(mi.p_full[i][0]), 4);
+      mbar_init(bar(mi.p_full[i][1]), 4);
       mbar_init(bar(mi.o_full[i]), 1);
     }
     for (int i = 0; i < kQueue; ++i) {
@@ -282,9 +331,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* ring = smem + S::OFF_RING;
 
   // Registers: 384 threads x 168 at launch; a softmax thread holds a row of
-  // scores: 2 x 128 x 208 + 128 x 80 of the 64512
+  // scores: 2 x 128 x 216 + 128 x 72 = 64512
   if (warp == 9) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     // ---------------- items and loads
     if (lane == 0) {
       prefetch_tmap(&tq);
@@ -391,106 +440,134 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_wait_bounded(bar(mi.full[p % S::NS]), (p / S::NS) & 1, kTimeoutNs);
     if (n_q > 0) mbar_wait_bounded(bar(mi.q_full), (n_q - 1) & 1, kTimeoutNs);
   } else if (warp == 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    // ---------------- products
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = umma_idesc_bf16(128, 128, false, false);
-      constexpr uint32_t idesc_o = umma_idesc_bf16(128, D, false, true);
-      int base = 0, it = 0, cs[2] = {0, 0};  // cs: P phases used by each tile
-      bool ok = true;
-      while (ok) {
-        const int e = it % kQueue;
-        if (!wait(mi.it_full[e], it / kQueue, 5)) break;
-        const Item& x = mi.items[e];
-        const int n = x.b1 - x.b0, np = x.t.np, jb = x.b0;
-        const bool end = x.b1 < 0, pair = (x.t.n_tok << a.lg) > 128;
-        mbar_arrive(bar(mi.it_empty[e]));
-        if (end) break;
-        auto issue_s = [&](int tile, int q, int pos) {
-          const uint32_t qa = smem_u32(smem + S::OFF_Q + q * S::TILE), ka = smem_u32(ring + (pos % S::NS) * S::TILE);
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    // ---------------- products.  The whole warp walks the blocks, one elected lane
+    // issues: what the products take (descriptors, addresses) then stays in uniform
+    // registers (a single-lane branch took 80-150 cycles to issue a 64-cycle product)
+    constexpr uint32_t idesc_s = umma_idesc_bf16(128, 128, false, false);
+    constexpr uint32_t idesc_o = umma_idesc_bf16(128, D, false, true);
+    auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    const uint32_t tm = (uint32_t)uni((int)tmem);
+    const uint32_t q_lo = (uint32_t)uni((int)(smem_u32(smem + S::OFF_Q) >> 4));
+    const uint32_t ring_lo = (uint32_t)uni((int)(smem_u32(ring) >> 4));
+    const bool lead = elect_one();
+    int base = 0, it = 0, c0 = 0, c1 = 0;  // c0, c1: P phases used of each tile
+    bool ok = true;
+    // S = Q K^T of Q tile q into score buffer `tile`, K in ring slot sl
+    auto issue_s = [&](int tile, int q, int sl) {
+      tc_fence_after();
+      const uint32_t qa = q_lo + q * (S::TILE >> 4), ka = ring_lo + sl * (S::TILE >> 4), d = tm + S::T_S + tile * 128;
+      if (lead) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            const uint64_t ad = umma_sdesc_sw128(qa + (k >> 2) * S::BLK + (k & 3) * 32, 1, 64);
-            const uint64_t bd = umma_sdesc_sw128(ka + (k >> 2) * S::BLK + (k & 3) * 32, 1, 64);
-            umma_bf16(tmem + S::T_S + tile * 128, ad, bd, idesc_s, k > 0 ? 1u : 0u);
-          }
-          umma_commit(bar(mi.s_full[tile]));
-        };
-        auto issue_o = [&](int tile, int j, int pos, bool first) {
-          const uint32_t va = smem_u32(ring + (pos % S::NS) * S::TILE);
-          const int pages = min(8, np - 8 * (jb + j));
-          for (int c = 0; c < pages; ++c)
-            umma_bf16_ts(tmem + S::T_O + tile * D, tmem + S::T_S + tile * 128 + 8 * c,
-                         umma_sdesc_sw128(va + c * 2048, S::BLK >> 4, 64), idesc_o, first && c == 0 ? 0u : 1u);
-        };
-        auto wait_load = [&](int pos) -> bool { return wait(mi.full[pos % S::NS], pos / S::NS, 6); };
-        if (!wait(mi.q_full, it, 7)) break;
-        if (pair) {
-          ok = wait_load(pos_k(base, 0));
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t o = (k >> 2) * (S::BLK >> 4) + (k & 3) * 2;
+          umma_bf16(d, sdesc_sw128_lo(qa + o, 1, 64), sdesc_sw128_lo(ka + o, 1, 64), idesc_s, k > 0 ? 1u : 0u);
+        }
+        umma_commit(bar(mi.s_full[tile]));
+      }
+      __syncwarp();
+    };
+    // O += P V, V in ring slot sl, the first four pages as soon as their weights are written
+    auto issue_o = [&](int tile, int sl, int pages, bool first, int phase) -> bool {
+      const uint32_t va = ring_lo + sl * (S::TILE >> 4), d = tm + S::T_O + tile * D, p = tm + S::T_S + tile * 128;
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        if (hf == 1 && !wwait(mi.p_full[tile][1], phase, 18)) return false;
+        tc_fence_after();
+        if (lead) {
+#pragma unroll
+          for (int c = 4 * hf; c < 4 * hf + 4; ++c)
+            if (c < pages)
+              umma_bf16_ts(d, p + 8 * c, sdesc_sw128_lo(va + c * 128, S::BLK >> 4, 64), idesc_o,
+                           first && c == 0 ? 0u : 1u);
+        }
+        __syncwarp();
+      }
+      return true;
+    };
+    auto commit = [&](uint64_t& b) {
+      if (lead) umma_commit(bar(b));
+      __syncwarp();
+    };
+    auto wait_load = [&](int pos) -> bool { return wwait(mi.full[pos % S::NS], pos / S::NS, 6); };
+    while (ok) {
+      const int e = it % kQueue;
+      if (!wwait(mi.it_full[e], it / kQueue, 5)) break;
+      const Item& x = mi.items[e];
+      const int b1 = uni(x.b1), jb = uni(x.b0), n = b1 - jb, np = uni(x.t.np);
+      const bool pair = (uni(x.t.n_tok) << a.lg) > 128;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(mi.it_empty[e]));
+      if (b1 < 0) break;
+      if (!wwait(mi.q_full, it, 7)) break;
+      if (pair) {
+        const int p0 = pos_k(base, 0);
+        if (!(ok = wait_load(p0))) break;
+        issue_s(0, 0, p0 % S::NS);
+        issue_s(1, 1, p0 % S::NS);
+        commit(mi.empty[p0 % S::NS]);
+        if (n == 1) commit(mi.q_empty);
+        for (int j = 0; j < n; ++j) {
+          const int pv = pos_v(base, j, n), pk = pos_k(base, j + 1), pages = min(8, np - 8 * (jb + j));
+          const bool more = j + 1 < n;
+          // tile 0
+          ok = wwait(mi.p_full[0][0], c0, 8) && wait_load(pv) && (j || it == 0 || wwait(mi.o_free, it - 1, 9)) &&
+               issue_o(0, pv % S::NS, pages, j == 0, c0);
           if (!ok) break;
-          tc_fence_after();
-          issue_s(0, 0, pos_k(base, 0));
-          issue_s(1, 1, pos_k(base, 0));
-          umma_commit(bar(mi.empty[pos_k(base, 0) % S::NS]));
-          if (n == 1) umma_commit(bar(mi.q_empty));
-          for (int j = 0; j < n && ok; ++j) {
-            const int pv = pos_v(base, j, n), pk = pos_k(base, j + 1);
-            for (int tile = 0; tile < 2 && ok; ++tile) {
-              ok = wait(mi.p_full[tile], cs[tile]++, 8) && (tile || wait_load(pv)) &&
-                   (tile || j || it == 0 || wait(mi.o_free, it - 1, 9));
-              if (!ok) break;
-              tc_fence_after();
-              issue_o(tile, j, pv, j == 0);
-              if (j == n - 1) umma_commit(bar(mi.o_full[tile]));
-              if (tile == 1) umma_commit(bar(mi.empty[pv % S::NS]));
-              if (j + 1 < n) {
-                if (!tile && !(ok = wait_load(pk))) break;
-                tc_fence_after();
-                issue_s(tile, tile, pk);
-                if (tile == 1) {
-                  umma_commit(bar(mi.empty[pk % S::NS]));
-                  if (j + 2 == n) umma_commit(bar(mi.q_empty));
-                }
-              }
-            }
-          }
-        } else {
-          for (int j = 0; j < min(n, 2) && ok; ++j) {
-            const int pk = pos_k(base, j);
+          ++c0;
+          if (more) {
             if (!(ok = wait_load(pk))) break;
-            tc_fence_after();
-            issue_s(j, 0, pk);
-            umma_commit(bar(mi.empty[pk % S::NS]));
-            if (j == n - 1) umma_commit(bar(mi.q_empty));
+            issue_s(0, 0, pk % S::NS);
+          } else {
+            commit(mi.o_full[0]);
           }
-          for (int j = 0; j < n && ok; ++j) {
-            const int tile = j & 1, pv = pos_v(base, j, n);
-            ok = wait(mi.p_full[tile], cs[tile]++, 10) && wait_load(pv) && (j || it == 0 || wait(mi.o_free, it - 1, 11));
-            if (!ok) break;
-            tc_fence_after();
-            issue_o(tile, j, pv, j < 2);
-            umma_commit(bar(mi.empty[pv % S::NS]));
-            if (j + 2 >= n) umma_commit(bar(mi.o_full[tile]));
-            if (j + 2 < n) {
-              const int pk = pos_k(base, j + 2);
-              if (!(ok = wait_load(pk))) break;
-              tc_fence_after();
-              issue_s(tile, 0, pk);
-              umma_commit(bar(mi.empty[pk % S::NS]));
-              if (j + 3 == n) umma_commit(bar(mi.q_empty));
-            }
+          // tile 1, which frees the slots
+          ok = wwait(mi.p_full[1][0], c1, 8) && issue_o(1, pv % S::NS, pages, j == 0, c1);
+          if (!ok) break;
+          ++c1;
+          commit(mi.empty[pv % S::NS]);
+          if (more) {
+            issue_s(1, 1, pk % S::NS);
+            commit(mi.empty[pk % S::NS]);
+            if (j + 2 == n) commit(mi.q_empty);
+          } else {
+            commit(mi.o_full[1]);
           }
         }
-        base += 2 * n;
-        ++it;
+      } else {
+        for (int j = 0; j < min(n, 2); ++j) {
+          const int pk = pos_k(base, j);
+          if (!(ok = wait_load(pk))) break;
+          issue_s(j, 0, pk % S::NS);
+          commit(mi.empty[pk % S::NS]);
+          if (j == n - 1) commit(mi.q_empty);
+        }
+        for (int j = 0; j < n && ok; ++j) {
+          const int tile = j & 1, pv = pos_v(base, j, n), pages = min(8, np - 8 * (jb + j));
+          const int phase = tile ? c1++ : c0++;
+          ok = wwait(mi.p_full[tile][0], phase, 10) && wait_load(pv) && (j || it == 0 || wwait(mi.o_free, it - 1, 11)) &&
+               issue_o(tile, pv % S::NS, pages, j < 2, phase);
+          if (!ok) break;
+          commit(mi.empty[pv % S::NS]);
+          if (j + 2 >= n) commit(mi.o_full[tile]);
+          if (j + 2 < n) {
+            const int pk = pos_k(base, j + 2);
+            if (!(ok = wait_load(pk))) break;
+            issue_s(tile, 0, pk % S::NS);
+            commit(mi.empty[pk % S::NS]);
+            if (j + 3 == n) commit(mi.q_empty);
+          }
+        }
       }
-      // every product issued has completed before the tensor memory is released
-      umma_commit(bar(mi.done));
-      mbar_wait_bounded(bar(mi.done), 0, kTimeoutNs);
+      base += 2 * n;
+      ++it;
     }
+    // every product issued has completed before the tensor memory is released
+    commit(mi.done);
+    mbar_wait_bounded(bar(mi.done), 0, kTimeoutNs);
     __syncwarp();
   } else if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // ---------------- softmax: group `grp`, row (= TMEM lane) quad * 32 + lane of its tile
     const int grp = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quad * 32) << 16;
@@ -539,16 +616,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int pg = 0; pg < 8; ++pg) {
             const int t0 = t.page_index(v0 + pg) * kPage;
             const bool gone = pg >= pages || (holes >> pg & 1);
-            const int top = gone ? -1 : p - t0;                                   // x <= top
-            const int low = a.w.window ? p - a.w.window - t0 : INT32_MIN, sk = a.w.sinks - t0;
+            // bit i: this row sees token t0 + i
+            const int top = p - t0, low = a.w.window ? p - a.w.window - t0 : -1, sk = a.w.sinks - t0;
+            const uint32_t upto = top < 0 ? 0u : 0xffffu >> (15 - min(top, 15));
+            const uint32_t from = low < 0 ? 0xffffu : 0xffffu << min(low + 1, 16);
+            const uint32_t sink = sk <= 0 ? 0u : 0xffffu >> (16 - min(sk, 16));
+            const uint32_t see = gone ? 0u : upto & (from | sink);
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (!(i <= top && (i > low || i < sk))) x[pg >> 1][16 * (pg & 1) + i] = -INFINITY;
+            for (int i = 0; i < 16; ++i) {
+              float& y = x[pg >> 1][16 * (pg & 1) + i];
+              y = see & (1u << i) ? y : -INFINITY;
+            }
           }
         }
-        float mx = -INFINITY;
+        float mq[4];
 #pragma unroll
-        for (int i = 0; i < 128; i += 2) mx = fmaxf(mx, fmaxf(x[i >> 5][i & 31], x[i >> 5][(i & 31) + 1]));
+        for (int c = 0; c < 4; ++c) {
+          mq[c] = x[c][0];
+#pragma unroll
+          for (int i = 1; i < 31; i += 2) mq[c] = max3(mq[c], x[c][i], x[c][i + 1]);
+        }
+        float mx = max3(max3(mq[0], mq[1], x[0][31]), max3(mq[2], mq[3], x[1][31]), fmaxf(x[2][31], x[3][31]));
         mx *= a.scale_log2;
         if (first) {
           m = mx;
@@ -571,20 +659,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         first = false;
         const float mc = m == -INFINITY ? 0.f : -m;
         const float2 sc = make_float2(a.scale_log2, a.scale_log2), mm = make_float2(mc, mc);
-        float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float pw[32];  // 16 words of two weights
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float2 y = ffma2(make_float2(x[c][i], x[c][i + 1]), sc, mm);
-            const float e0 = ex2(y.x), e1 = ex2(y.y);
-            sum = ffma2(make_float2(e0, e1), make_float2(1.f, 1.f), sum);
-            pw[i >> 1] = __uint_as_float(pack_bf16x2(e0, e1));
-          }
-          tmem_st16<0>(t_s + 16 * c, pw);
-        }
-        l += sum.x + sum.y;
         // tokens that no row of the item sees (past the session's end, between the
         // sinks and the first window) may hold anything: a weight of 0 times NaN is
         // NaN, so their V rows are zeroed; the first tile of a pair does it for both
@@ -605,10 +679,36 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async_smem();
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(mi.p_full[grp]));
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        // weights of 32 keys, 16 words of two
+        auto chunk = [&](auto fma_tag, float(&y)[32], int c) {
+          constexpr bool FMA = decltype(fma_tag)::value;
+          float pw[32];
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float2 z = ffma2(make_float2(y[i], y[i + 1]), sc, mm);
+            const bool fma = FMA && (i >> 1) % (16 / kFmaPairs) == 16 / kFmaPairs - 1;
+            const float2 e = fma ? exp2_fma(z) : make_float2(ex2(z.x), ex2(z.y));
+            sum[(i >> 1) & 1] = fadd2(sum[(i >> 1) & 1], e);
+            pw[i >> 1] = __uint_as_float(pack_bf16x2(e.x, e.y));
+          }
+          tmem_st16<0>(t_s + 16 * c, pw);
+        };
+        auto weights = [&](auto fma_tag) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            chunk(fma_tag, x[2 * hf], 2 * hf);
+            chunk(fma_tag, x[2 * hf + 1], 2 * hf + 1);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(mi.p_full[grp][hf]));
+          }
+        };
+        // masked scores are -inf, which only ex2 takes
+        if (all) weights(std::true_type{});
+        else weights(std::false_type{});
+        l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
       }
       if (!ok) break;
       // ---------------- the item's end
@@ -691,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++it;
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   }
   tc_fence_before();
   __syncthreads();
