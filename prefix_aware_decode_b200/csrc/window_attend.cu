@@ -28,8 +28,6 @@
 // written over S, O += P V (TMEM).  The running maximum is raised, and O
 // rescaled, only when it grows by more than 2^8: numerator and denominator use
 // the same maximum, so the result is unchanged.
-#include <type_traits>
-
 #include "ptx.cuh"
 #include "sessions.cuh"
 #include "tmap.h"
@@ -42,7 +40,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kThreads = 384;
 constexpr int kMaxChunks = 256;      // chunks of kThreads tile slots that a CTA sums
 constexpr int kQueue = 2;            // entries of the CTA's item queue
-constexpr int kFmaPairs = 4;           // of the 16 pairs of scores of a 32-key chunk: exponentials on the FMA pipe
+constexpr int kParts = 2;              // parts of a block's weights that are handed over one by one
 constexpr float kRaise = 8.f;        // log2 growth of a maximum that raises it
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
@@ -138,7 +136,7 @@ static_assert(Shape<128>::SMEM <= 232448 && Shape<64>::SMEM <= 232448, "shared m
 struct Misc {
   uint64_t full[8], empty[8];          // ring
   uint64_t q_full, q_empty, o_free, joined, done;
-  uint64_t s_full[2], p_full[2][2], o_full[2];  // p_full: by tile and half of the block's keys
+  uint64_t s_full[2], p_full[2][kParts], o_full[2];  // p_full: by tile and part of the block's keys
   uint64_t it_full[kQueue], it_empty[kQueue];
   uint32_t tmem;
   int fail;
@@ -180,24 +178,20 @@ __device__ __forceinline__ uint64_t sdesc_sw128_lo(uint32_t addr16, uint32_t lbo
   return (uint64_t)(addr16 | (lbo16 << 16)) | ((uint64_t)(sbo16 | (1u << 14) | (2u << 29)) << 32);
 }
 
-// 2^x of two finite x <= 127 on the FMA pipe: x = n + f, f in [-1/2, 1/2]; 2^f by
-// the degree-5 polynomial of least relative error (Remez exchange, 7.5e-8), n
-// added to the exponent.  x below -126 counts as -126.
-__device__ __forceinline__ float2 exp2_fma(float2 x) {
-  x.x = fmaxf(x.x, -126.f);
-  x.y = fmaxf(x.y, -126.f);
-  const float2 big = make_float2(12582912.f, 12582912.f);  // 1.5 * 2^23: adding it rounds to an integer
-  const float2 t = fadd2(x, big);
-  const float2 f = fadd2(x, fmul2(fadd2(t, make_float2(-12582912.f, -12582912.f)), make_float2(-1.f, -1.f)));
-  float2 p = make_float2(1.3276472454890609e-3f, 1.3276472454890609e-3f);
-  p = ffma2(p, f, make_float2(9.675540961325169e-3f, 9.675540961325169e-3f));
-  p = ffma2(p, f, make_float2(5.550713092088699e-2f, 5.550713092088699e-2f));
-  p = ffma2(p, f, make_float2(0.24022120237350464f, 0.24022120237350464f));
-  p = ffma2(p, f, make_float2(0.6931469440460205f, 0.6931469440460205f));
-  p = ffma2(p, f, make_float2(1.0000001192092896f, 1.0000001192092896f));
-  p.x = __uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23));
-  p.y = __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23));
-  return p;
+// Whole warp: 8 fp32 columns of its 32 TMEM lanes times each lane's f.
+__device__ __forceinline__ void tmem_scale8(uint32_t taddr, float f) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 template <int D>
@@ -287,8 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(mi.done), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(mi.s_full[i]), 1);
-      mbar_init(bar(mi.p_full[i][0]), 4);
-      mbar_init(bar(mi.p_full[i][1]), 4);
+      for (int c = 0; c < kParts; ++c) mbar_init(bar(mi.p_full[i][c]), 4);
       mbar_init(bar(mi.o_full[i]), 1);
     }
     for (int i = 0; i < kQueue; ++i) {
@@ -307,23 +300,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = mi.tmem;
   volatile int* fail = &mi.fail;
 
-  // Wait for a phase; gives up after kTimeoutNs, or when another role has.
-  auto wait = [&](uint64_t& b, int phase, int code) -> bool {
+  // A whole warp waits for a phase; false when that took kTimeoutNs, or when
+  // another role has given up.  A phase that is over costs one vote: the branch
+  // is uniform (a loop that lanes leave one by one took 100 cycles).
+  auto wwait = [&](uint64_t& b, int phase, int code) -> bool {
     const uint32_t ad = bar(b), par = (uint32_t)phase & 1u;
-    if (mbar_try_wait(ad, par)) return true;
+    if (__all_sync(0xffffffffu, mbar_try_wait(ad, par))) return true;
     const uint64_t t0 = global_timer_ns();
-    for (;;) {
-      if (mbar_try_wait(ad, par)) return true;
-      if (*fail) return false;
-      if (global_timer_ns() - t0 > kTimeoutNs) {
-        *fail = 1;
-        record_status(a.status, PA_ERR_TIMEOUT, blockIdx.x, code);
+    while (!__all_sync(0xffffffffu, mbar_try_wait(ad, par))) {
+      if (__any_sync(0xffffffffu, *fail != 0)) return false;
+      if (__any_sync(0xffffffffu, global_timer_ns() - t0 > kTimeoutNs)) {
+        if (lane == 0) {
+          *fail = 1;
+          record_status(a.status, PA_ERR_TIMEOUT, blockIdx.x, code);
+        }
         return false;
       }
     }
+    return true;
   };
-  // The same by a whole warp: all lanes succeed or none does.
-  auto wwait = [&](uint64_t& b, int phase, int code) -> bool { return __all_sync(0xffffffffu, wait(b, phase, code)); };
   // Ring position of the loads of a segment of n blocks whose first load is
   // number `base`: K0 K1 V0 K2 V1 ... V(n-1), the order in which they are used.
   auto pos_k = [](int base, int j) { return j == 0 ? base : base + 2 * j - 1; };
@@ -467,19 +462,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     };
-    // O += P V, V in ring slot sl, the first four pages as soon as their weights are written
+    // O += P V, V in ring slot sl, part by part as the weights are written
     auto issue_o = [&](int tile, int sl, int pages, bool first, int phase) -> bool {
       const uint32_t va = ring_lo + sl * (S::TILE >> 4), d = tm + S::T_O + tile * D, p = tm + S::T_S + tile * 128;
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        if (hf == 1 && !wwait(mi.p_full[tile][1], phase, 18)) return false;
+      for (int part = 0; part < kParts; ++part) {
+        if (part > 0 && !wwait(mi.p_full[tile][part], phase, 18)) return false;
         tc_fence_after();
+        auto pv = [&](int c) {
+          umma_bf16_ts(d, p + 8 * c, sdesc_sw128_lo(va + c * 128, S::BLK >> 4, 64), idesc_o, first && c == 0 ? 0u : 1u);
+        };
         if (lead) {
+          if (pages == 8) {
 #pragma unroll
-          for (int c = 4 * hf; c < 4 * hf + 4; ++c)
-            if (c < pages)
-              umma_bf16_ts(d, p + 8 * c, sdesc_sw128_lo(va + c * 128, S::BLK >> 4, 64), idesc_o,
-                           first && c == 0 ? 0u : 1u);
+            for (int c = 8 / kParts * part; c < 8 / kParts * (part + 1); ++c) pv(c);
+          } else {
+            for (int c = 8 / kParts * part; c < min(pages, 8 / kParts * (part + 1)); ++c) pv(c);
+          }
         }
         __syncwarp();
       }
@@ -511,12 +510,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int pv = pos_v(base, j, n), pk = pos_k(base, j + 1), pages = min(8, np - 8 * (jb + j));
           const bool more = j + 1 < n;
           // tile 0
-          ok = wwait(mi.p_full[0][0], c0, 8) && wait_load(pv) && (j || it == 0 || wwait(mi.o_free, it - 1, 9)) &&
-               issue_o(0, pv % S::NS, pages, j == 0, c0);
+          // (what does not depend on the weights is waited for first: the way from a
+          // tile's last weights to its next scores is what a block costs)
+          ok = wait_load(pv) && (!more || wait_load(pk)) && (j || it == 0 || wwait(mi.o_free, it - 1, 9)) &&
+               wwait(mi.p_full[0][0], c0, 8) && issue_o(0, pv % S::NS, pages, j == 0, c0);
           if (!ok) break;
           ++c0;
           if (more) {
-            if (!(ok = wait_load(pk))) break;
             issue_s(0, 0, pk % S::NS);
           } else {
             commit(mi.o_full[0]);
@@ -525,12 +525,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wwait(mi.p_full[1][0], c1, 8) && issue_o(1, pv % S::NS, pages, j == 0, c1);
           if (!ok) break;
           ++c1;
-          commit(mi.empty[pv % S::NS]);
           if (more) {
             issue_s(1, 1, pk % S::NS);
+            commit(mi.empty[pv % S::NS]);
             commit(mi.empty[pk % S::NS]);
             if (j + 2 == n) commit(mi.q_empty);
           } else {
+            commit(mi.empty[pv % S::NS]);
             commit(mi.o_full[1]);
           }
         }
@@ -545,17 +546,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < n && ok; ++j) {
           const int tile = j & 1, pv = pos_v(base, j, n), pages = min(8, np - 8 * (jb + j));
           const int phase = tile ? c1++ : c0++;
-          ok = wwait(mi.p_full[tile][0], phase, 10) && wait_load(pv) && (j || it == 0 || wwait(mi.o_free, it - 1, 11)) &&
-               issue_o(tile, pv % S::NS, pages, j < 2, phase);
+          const bool more = j + 2 < n;
+          const int pk = pos_k(base, j + 2);
+          ok = wait_load(pv) && (j || it == 0 || wwait(mi.o_free, it - 1, 11)) && wwait(mi.p_full[tile][0], phase, 10) &&
+               issue_o(tile, pv % S::NS, pages, j < 2, phase) && (!more || wait_load(pk));
           if (!ok) break;
-          commit(mi.empty[pv % S::NS]);
-          if (j + 2 >= n) commit(mi.o_full[tile]);
-          if (j + 2 < n) {
-            const int pk = pos_k(base, j + 2);
-            if (!(ok = wait_load(pk))) break;
+          if (more) {
             issue_s(tile, 0, pk % S::NS);
+            commit(mi.empty[pv % S::NS]);
             commit(mi.empty[pk % S::NS]);
             if (j + 3 == n) commit(mi.q_empty);
+          } else {
+            commit(mi.empty[pv % S::NS]);
+            commit(mi.o_full[tile]);
           }
         }
       }
@@ -589,6 +592,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int p = t.p0 + min(tok, t.n_tok - 1);        // rows past the tile repeat its last
       const int p_min = t.p0 + tok0, p_max = t.p0 + min(tok0 + (128 >> a.lg), t.n_tok) - 1;
       const int kv_end = a.b.kv_len(t.s), seen_from = a.w.first(max(t.p0, 0));
+      // a warp without rows keeps the protocol and leaves its rows of P and O as they are
+      const bool busy = __any_sync(0xffffffffu, tok < t.n_tok);
       // the page (or hole, -1) of lane's page of block j, asked for a block ahead
       auto page_of = [&](int j) -> int {
         const int v = 8 * (b0 + j) + lane;
@@ -604,8 +609,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t_first = t.page_index(v0) * kPage, t_last = t.page_index(v0 + pages - 1) * kPage + kPage - 1;
         const bool all = pages == 8 && holes == 0 && t_last <= p_min &&
                          (a.w.window == 0 || (v0 >= t.ns && t_first > p_max - a.w.window) || t_last < a.w.sinks);
+        // tokens that no row of the item sees (past the session's end, between the
+        // sinks and the first window) may hold anything: a weight of 0 times NaN is
+        // NaN, so their V rows are zeroed; the first tile of a pair does it for both
+        bool dead = false;
+        if (!all && lane < pages) {
+          const int t0 = t.page_index(v0 + lane) * kPage;
+          dead = t0 + kPage > kv_end || (t0 + kPage > a.w.sinks && t0 < seen_from);
+        }
+        if (__any_sync(0xffffffffu, dead) && (grp == 0 || !pair)) {
+          const int pv = pos_v(base, j, n);
+          if (!(ok = wwait(mi.full[pv % S::NS], pv / S::NS, 14))) break;
+          const int key = tid & 127, tk0 = t.page_index(v0 + (key >> 4)) * kPage + (key & 15);
+          if ((key >> 4) < pages && (tk0 >= kv_end || (tk0 >= a.w.sinks && tk0 < seen_from))) {
+            uint8_t* vt = ring + (pv % S::NS) * S::TILE + key * 128;
+#pragma unroll
+            for (int i = 0; i < 8 * S::HALVES; ++i)
+              *reinterpret_cast<uint4*>(vt + (i >> 3) * S::BLK + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
         if (!(ok = wwait(mi.s_full[grp], ps++, 13))) break;
         tc_fence_after();
+        if (!busy) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0)
+            for (int i = 0; i < kParts; ++i) mbar_arrive(bar(mi.p_full[grp][i]));
+          continue;
+        }
         float x[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, x[c]);
@@ -646,68 +678,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           l *= f;
           m = mn;
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            float o[32];
-            tmem_ld32(t_o + c, o);
-            tmem_wait_ld_into(o);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= f;
-            tmem_st32(t_o + c, o);
-          }
+          for (int c = 0; c < D; c += 8) tmem_scale8(t_o + c, f);
           tmem_wait_st();
         }
         first = false;
         const float mc = m == -INFINITY ? 0.f : -m;
         const float2 sc = make_float2(a.scale_log2, a.scale_log2), mm = make_float2(mc, mc);
-        // tokens that no row of the item sees (past the session's end, between the
-        // sinks and the first window) may hold anything: a weight of 0 times NaN is
-        // NaN, so their V rows are zeroed; the first tile of a pair does it for both
-        bool dead = false;
-        if (lane < pages) {
-          const int t0 = t.page_index(v0 + lane) * kPage;
-          dead = t0 + kPage > kv_end || (t0 + kPage > a.w.sinks && t0 < seen_from);
-        }
-        if (__any_sync(0xffffffffu, dead) && (grp == 0 || !pair)) {
-          const int pv = pos_v(base, j, n);
-          if (!(ok = wwait(mi.full[pv % S::NS], pv / S::NS, 14))) break;
-          const int key = tid & 127, tk0 = t.page_index(v0 + (key >> 4)) * kPage + (key & 15);
-          if ((key >> 4) < pages && (tk0 >= kv_end || (tk0 >= a.w.sinks && tk0 < seen_from))) {
-            uint8_t* vt = ring + (pv % S::NS) * S::TILE + key * 128;
-#pragma unroll
-            for (int i = 0; i < 8 * S::HALVES; ++i)
-              *reinterpret_cast<uint4*>(vt + (i >> 3) * S::BLK + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-        }
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // weights of 32 keys, 16 words of two
-        auto chunk = [&](auto fma_tag, float(&y)[32], int c) {
-          constexpr bool FMA = decltype(fma_tag)::value;
+        // the weights, 32 keys (16 words of two) at a time
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
           float pw[32];
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            const float2 z = ffma2(make_float2(y[i], y[i + 1]), sc, mm);
-            const bool fma = FMA && (i >> 1) % (16 / kFmaPairs) == 16 / kFmaPairs - 1;
-            const float2 e = fma ? exp2_fma(z) : make_float2(ex2(z.x), ex2(z.y));
-            sum[(i >> 1) & 1] = fadd2(sum[(i >> 1) & 1], e);
-            pw[i >> 1] = __uint_as_float(pack_bf16x2(e.x, e.y));
+            const float2 z = ffma2(make_float2(x[c][i], x[c][i + 1]), sc, mm);
+            const float2 y = make_float2(ex2(z.x), ex2(z.y));
+            sum[(i >> 1) & 1] = fadd2(sum[(i >> 1) & 1], y);
+            pw[i >> 1] = __uint_as_float(pack_bf16x2(y.x, y.y));
           }
           tmem_st16<0>(t_s + 16 * c, pw);
-        };
-        auto weights = [&](auto fma_tag) {
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            chunk(fma_tag, x[2 * hf], 2 * hf);
-            chunk(fma_tag, x[2 * hf + 1], 2 * hf + 1);
+          if ((c + 1) % (4 / kParts) == 0) {
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(mi.p_full[grp][hf]));
+            if (lane == 0) mbar_arrive(bar(mi.p_full[grp][(c + 1) / (4 / kParts) - 1]));
           }
-        };
-        // masked scores are -inf, which only ex2 takes
-        if (all) weights(std::true_type{});
-        else weights(std::false_type{});
+        }
         l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
       }
       if (!ok) break;
