@@ -473,6 +473,11 @@ pa_status pa_window_status(const void *d_workspace, void *stream, pa_status *out
 pa_status pa_weigh_tokens(const pa_sessions *b, int32_t window, int32_t sinks, float softmax_scale, const void *q,
                           const void *k_pool, const float *lse, float *scores, int64_t max_tokens, void *stream);
 
+/* The first failure of a device-side bounded wait of pa_weigh_tokens on the
+ * current device since this call last returned one (PA_OK: none); scores of that
+ * time are then not to be used.  Synchronises `stream`. */
+pa_status pa_weigh_status(void *stream, pa_status *out);
+
 /*
  * Evict: every (session, kv head) keeps its first `sinks` and last `recent`
  * tokens and the highest-scoring of the rest, `budget` tokens in all (all of

@@ -8,7 +8,7 @@ from ._binding import (PA_ERR_CUDA, PA_ERR_DEVICE, PA_ERR_INVALID, PA_ERR_NOMEM,
                        PA_PLAN_FAULT_DROP_LOAD, PA_PLAN_KEEP_PACK, PA_PLAN_NO_SHARING, DecodeStep, PaError, PaImageHeader, Plan, attend, merge_rows,
                        lib)
 
-_CACHE_OPS = ("evict_tokens", "rope_append", "weigh_tokens", "window_attend", "window_status", "window_workspace")
+_CACHE_OPS = ("evict_tokens", "rope_append", "weigh_status", "weigh_tokens", "window_attend", "window_status", "window_workspace")
 
 
 def __getattr__(name):

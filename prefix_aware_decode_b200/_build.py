@@ -22,7 +22,7 @@ LIB = os.path.join(HERE, "libpa.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CU_SOURCES = ["kernels.cu", "capi.cu", "noalloc.cu", "rope_append.cu", "window_attend.cu", "weigh.cu", "evict.cu"]
 CPP_SOURCES = ["plan.cpp"]
-HEADERS = ["plan.h", "ptx.cuh", "sessions.cuh", "tmap.h"]
+HEADERS = ["plan.h", "ptx.cuh", "sessions.cuh", "tmap.h", "umma.cuh"]
 
 
 def nvcc() -> str:

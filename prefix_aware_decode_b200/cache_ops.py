@@ -239,6 +239,16 @@ def weigh_tokens(q, k_pool, lse, block_table, kv_lens, cu_rows, scores, *, windo
     return scores
 
 
+def weigh_status(device=None, stream=None) -> int:
+    """The first failure of a bounded wait of weigh_tokens on the device since this
+    call last returned one (pa_weigh_status; PA_OK: none).  Synchronises the stream."""
+    out = ctypes.c_int()
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with _Call(device, stream) as cs:
+        _check(lib().pa_weigh_status(cs, ctypes.byref(out)), "pa_weigh_status")
+    return out.value
+
+
 def evict_tokens(scores, k_pool, v_pool, block_table, kv_lens, dst_table, budget: int, *, sinks: int = 0,
                  recent: int = 0, scores_out=None, stream=None):
     """Keeps, per (session, kv head), the first `sinks`, the last `recent` and the

@@ -31,6 +31,7 @@
 #include "ptx.cuh"
 #include "sessions.cuh"
 #include "tmap.h"
+#include "umma.cuh"
 
 namespace pa {
 namespace {
@@ -152,31 +153,6 @@ struct Sums {
   long long lo_rest;
   int lo_slot, pad;
 };
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;"
-      : "=l"(d)
-      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
-  return *reinterpret_cast<float2*>(&d);
-}
-
-// One lane of a converged warp, the same one every time.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
-  return p != 0;
-}
-
-// umma_sdesc_sw128 from an address already in 16-byte units.
-__device__ __forceinline__ uint64_t sdesc_sw128_lo(uint32_t addr16, uint32_t lbo16, uint32_t sbo16) {
-  return (uint64_t)(addr16 | (lbo16 << 16)) | ((uint64_t)(sbo16 | (1u << 14) | (2u << 29)) << 32);
-}
 
 // Whole warp: 8 fp32 columns of its 32 TMEM lanes times each lane's f.
 __device__ __forceinline__ void tmem_scale8(uint32_t taddr, float f) {
@@ -792,6 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (*fail) settle();
   griddep_launch_dependents();
   if (warp == 8) tmem_free(tmem, 512);
 }

@@ -169,8 +169,8 @@ def test_captured_calls_follow_the_device_arrays(n_rows):
 # ------------------------------------------------------------------------------------------------ weights
 
 
-def _weigh_case(kv, rows, Hq, Hkv, D, window, sinks, seed=0, holes=(), max_tokens=None):
-    c = Cache(kv, rows, Hq, Hkv, D, seed=seed, holes=holes, extra_rows=1)
+def _weigh_case(kv, rows, Hq, Hkv, D, window, sinks, seed=0, holes=(), max_tokens=None, extra_pages=1):
+    c = Cache(kv, rows, Hq, Hkv, D, seed=seed, holes=holes, extra_rows=1, extra_pages=extra_pages)
     _, lse = ref.run_attend(c, window, sinks)
     T = max_tokens or c.width * P
     s0 = torch.rand(len(kv), Hkv, T, generator=c.gen)
@@ -206,8 +206,18 @@ def test_weigh_head_layouts(batch, heads):
 def test_weigh_long_holes_and_a_short_score_row():
     _weigh_case([9000, 4100], [1, 3], 8, 1, 128, 0, 0, seed=23)
     _weigh_case([3000], [700], 4, 2, 128, 512, 16, seed=24)
+    _weigh_case([2500, 1900], [1300, 900], 8, 4, 64, 0, 0, seed=29, extra_pages=1000)
     _weigh_case([200, 150], [30, 1], 8, 2, 64, 0, 0, seed=25, holes=[(0, 0), (0, 5), (1, 3), (0, 12)])
     _weigh_case([200, 150], [30, 1], 8, 2, 64, 0, 0, seed=26, max_tokens=77)
+
+
+@gpu
+@pytest.mark.parametrize("heads", [(32, 8, 128), (8, 8, 64)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (150, 10)])
+@pytest.mark.parametrize("batch", list(BATCHES))
+def test_weigh_in_a_wide_table(batch, window, sinks, heads):
+    # a table wide enough that the kernel takes key blocks in pairs
+    _weigh_case(*BATCHES[batch], *heads, window, sinks, seed=28, extra_pages=700)
 
 
 @gpu
