@@ -216,7 +216,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 17) {
     // ---------------- items and loads
-    if (lane == 0) {
+    const bool lead = elect_one();
+    if (lead) {
       prefetch_tmap(&tq);
       prefetch_tmap(&tk);
     }
@@ -292,16 +293,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row = pg < 0 ? oob : (pg * a.b.Hkv + g) * kPage;
       for (int b = 0; b < a.pair && v0 + 8 * b < x.np; ++b) {
         const int np = min(8, x.np - v0 - 8 * b);
-        const int rw = __shfl_sync(0xffffffffu, row, (lane & 7) + 8 * b);
         if (kr.phase > 0 && !(ok = wwait(mi.kempty[kr.slot], kr.phase - 1, 2))) break;
-        if (lane == 0) mbar_arrive_expect_tx(bar(mi.kfull[kr.slot]), (uint32_t)np * kPage * D * 2);
-        __syncwarp();
+        load_pages<S::HALVES>(smem_u32(k_tile(kr.slot)), &tk, row, 8 * b, np, bar(mi.kfull[kr.slot]), lead);
         ++n_k;
-        if (lane < np) {
-          const uint32_t dst = smem_u32(k_tile(kr.slot)) + lane * 2048;
-#pragma unroll
-          for (int h = 0; h < S::HALVES; ++h) tma_load_2d(dst + h * S::BLK, &tk, 64 * h, rw, bar(mi.kfull[kr.slot]));
-        }
         kr.next(a.nk);
       }
       if (!ok) break;
@@ -318,8 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (qr.phase > 0 && !(ok = wwait(mi.qempty[qr.slot], qr.phase - 1, 3))) break;
           const uint32_t fb = bar(mi.qfull[qr.slot]);
-          if (lane == 0) {
+          if (lead) {
             mbar_arrive_expect_tx(fb, S::TILE);
+#pragma unroll
             for (int h = 0; h < S::HALVES; ++h)
               tma_load_3d(smem_u32(q_tile(qr.slot) + h * S::BLK), &tq, 64 * h, g << a.lg, x.r0 + tok, fb);
           }

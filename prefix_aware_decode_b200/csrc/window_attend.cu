@@ -306,7 +306,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     // ---------------- items and loads
-    if (lane == 0) {
+    const bool lead = elect_one();
+    if (lead) {
       prefetch_tmap(&tq);
       prefetch_tmap(&tk);
       prefetch_tmap(&tv);
@@ -349,13 +350,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (it > 0 && !wwait(mi.q_empty, it - 1, 2)) break;
       const bool pair = (t.n_tok << a.lg) > 128;
       ++n_q;
-      if (lane == 0) {
+      if (lead) {
         mbar_arrive_expect_tx(bar(mi.q_full), (pair ? 2 : 1) * S::TILE);
         for (int i = 0; i < (pair ? 2 : 1); ++i)
+#pragma unroll
           for (int h = 0; h < S::HALVES; ++h)
             tma_load_3d(smem_u32(smem + S::OFF_Q + i * S::TILE + h * S::BLK), &tq, 64 * h, g << a.lg,
                         t.r0 + i * (128 >> a.lg), bar(mi.q_full));
       }
+      __syncwarp();
       // rows of the pool of the block's pages, lane l < 8: page 8 j + l
       auto rows_of = [&](int j) -> int {
         const int v = 8 * j + lane;
@@ -366,15 +369,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto load = [&](int pos, const CUtensorMap* tm, int j, int row) -> bool {
         const int sl = pos % S::NS;
         if (pos >= S::NS && !wwait(mi.empty[sl], pos / S::NS - 1, 3)) return false;
-        const int np = min(8, t.np - 8 * j);
         issued = pos + 1;
-        if (lane == 0) mbar_arrive_expect_tx(bar(mi.full[sl]), (uint32_t)np * kPage * D * 2);
-        __syncwarp();
-        if (lane < np) {
-          const uint32_t dst = smem_u32(ring + sl * S::TILE) + lane * 2048;
-#pragma unroll
-          for (int h = 0; h < S::HALVES; ++h) tma_load_2d(dst + h * S::BLK, tm, 64 * h, row, bar(mi.full[sl]));
-        }
+        load_pages<S::HALVES>(smem_u32(ring + sl * S::TILE), tm, row, 0, min(8, t.np - 8 * j), bar(mi.full[sl]), lead);
         return true;
       };
       int row = rows_of(b0), prev = row;
