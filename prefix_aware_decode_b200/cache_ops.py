@@ -21,105 +21,147 @@ import torch
 
 from ._binding import PaRope, PaSessions, _check, lib
 
+_ref = ctypes.byref
 _I32, _F32, _F64, _BF16 = torch.int32, torch.float32, torch.float64, torch.bfloat16
+_Tensor, _empty = torch.Tensor, torch.empty
 
 
-def _ptr(t, name: str, dtype, device, align: int = 16) -> int:
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
-        raise ValueError(f"{name} must be a {dtype} tensor")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, the pools' device")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    p = t.data_ptr()
-    if p % align:
+def _ptr(t, name: str, dtype, index: int, align: int = 16) -> int:
+    """Address of a contiguous tensor of one type on CUDA device `index`."""
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.is_contiguous() and t.get_device() == index:
+        p = t.data_ptr()
+        if p % align == 0:
+            return p
         raise ValueError(f"{name} must be {align}-byte aligned")
-    return p
+    if not isinstance(t, _Tensor) or t.dtype is not dtype:
+        raise ValueError(f"{name} must be a {dtype} tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on the pools' device")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _rows_ptr(t, name: str, heads: int, rows: int, D: int, device) -> Tuple[int, int]:
+def _rows_ptr(t, name: str, heads: int, rows: int, D: int, index: int) -> Tuple[int, int]:
     """Address and row stride of [rows][heads][D] rows, which may be slices of wider ones."""
-    if not isinstance(t, torch.Tensor) or t.dtype != _BF16 or tuple(t.shape) != (rows, heads, D):
+    if not isinstance(t, _Tensor) or t.dtype is not _BF16 or t.shape != (rows, heads, D):
         raise ValueError(f"{name} must be a bf16 tensor [{rows}][{heads}][{D}]")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, the pools' device")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on the pools' device")
     s = t.stride()
     if (D > 1 and s[2] != 1) or (heads > 1 and s[1] != D):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
     stride = s[0] if rows > 1 else heads * D
-    if stride < heads * D or stride % 8 or t.data_ptr() % 16:
+    p = t.data_ptr()
+    if stride < heads * D or stride % 8 or p % 16:
         raise ValueError(f"{name}: rows must not overlap and must be 16-byte aligned")
-    return t.data_ptr(), stride
+    return p, stride
 
 
-class _Call:
-    """The device and stream of a call, made current for its launches and allocations."""
+class _On:
+    """Makes a device, or a stream of it, current for a call's launches and allocations."""
 
-    def __init__(self, device, stream):
-        if device.type != "cuda":
-            raise ValueError("the pools must be CUDA tensors")
+    def __init__(self, index: int, stream):
+        device = torch.device("cuda", index)
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=device)
         if stream is not None and stream.device != device:
             raise ValueError(f"stream must be a stream of {device}")
-        self.device, self.stream, self.ctx = device, stream, None
+        self.ctx = torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
 
-    def __enter__(self) -> int:
-        if self.stream is not None:
-            self.ctx = torch.cuda.stream(self.stream)
-        elif self.device.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(self.device)
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+    def __enter__(self):
+        self.ctx.__enter__()
 
     def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+        self.ctx.__exit__(*exc)
 
 
-def _sessions(k_pool, block_table, kv_lens, cu_rows, num_rows: int, num_q_heads: Optional[int]) -> PaSessions:
-    if not isinstance(k_pool, torch.Tensor) or k_pool.dim() != 4:
+class _Here:
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        pass
+
+
+_HERE = _Here()
+
+
+def _on(index: int, stream):
+    if stream is None and index == torch.cuda.current_device():
+        return _HERE
+    return _On(index, stream)
+
+
+def _current(index: int) -> int:
+    """The device's current stream (cudaStream_t); the private call costs a thirtieth of the public one."""
+    return _raw_stream(index)
+
+
+try:
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+except AttributeError:  # not in this torch
+    def _raw_stream(index: int) -> int:
+        return torch.cuda.current_stream(index).cuda_stream
+
+
+def _index(k_pool) -> int:
+    """The device of a call: k_pool's."""
+    if not isinstance(k_pool, _Tensor) or k_pool.dim() != 4:
         raise ValueError("k_pool must be a tensor [num_pages][Hkv][P][D]")
-    dev = k_pool.device
+    if not k_pool.is_cuda:
+        raise ValueError("k_pool must be a CUDA tensor")
+    return k_pool.get_device()
+
+
+def _sessions(k_pool, block_table, kv_lens, cu_rows, num_rows: int, num_q_heads: Optional[int], index: int) -> PaSessions:
     num_pages, Hkv, P, D = k_pool.shape
-    bt = _ptr(block_table, "block_table", _I32, dev, 4)
+    bt = _ptr(block_table, "block_table", _I32, index, 4)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [S][max_pages]")
     S, max_pages = block_table.shape
-    kv = _ptr(kv_lens, "kv_lens", _I32, dev, 4)
-    if tuple(kv_lens.shape) != (S,):
+    kv = _ptr(kv_lens, "kv_lens", _I32, index, 4)
+    if kv_lens.shape != (S,):
         raise ValueError("kv_lens must be [S], S the rows of block_table")
-    cu = None
-    if cu_rows is not None:
-        cu = _ptr(cu_rows, "cu_rows", _I32, dev, 4)
-        if tuple(cu_rows.shape) != (S + 1,):
-            raise ValueError("cu_rows must be [S + 1], S the rows of block_table")
-    return PaSessions(S, num_rows, Hkv if num_q_heads is None else num_q_heads, Hkv, D, P, max_pages, num_pages, bt, kv,
-                      cu)
+    if num_q_heads is None:
+        return PaSessions(S, 0, Hkv, Hkv, D, P, max_pages, num_pages, bt, kv, None)
+    cu = _ptr(cu_rows, "cu_rows", _I32, index, 4)
+    if cu_rows.shape != (S + 1,):
+        raise ValueError("cu_rows must be [S + 1], S the rows of block_table")
+    return PaSessions(S, num_rows, num_q_heads, Hkv, D, P, max_pages, num_pages, bt, kv, cu)
 
 
-def _pools(k_pool, v_pool) -> Tuple[int, int]:
-    dev = k_pool.device
+def _v_ptr(v_pool, k_pool, index: int) -> int:
+    p = _ptr(v_pool, "v_pool", _BF16, index)
     if v_pool.shape != k_pool.shape:
         raise ValueError("v_pool must have k_pool's shape")
-    return _ptr(k_pool, "k_pool", _BF16, dev), _ptr(v_pool, "v_pool", _BF16, dev)
+    return p
 
 
-def _q(q, D: int, device) -> int:
-    if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[2] != D:
+def _q_ptr(q, k_pool, index: int) -> int:
+    p = _ptr(q, "q", _BF16, index)
+    if q.dim() != 3 or q.shape[2] != k_pool.shape[3]:
         raise ValueError("q must be [rows][Hq][D], D that of the pools")
-    return _ptr(q, "q", _BF16, device)
+    return p
 
 
-def _out(t, name: str, shape, dtype, device, align: int = 16):
+def _out(t, name: str, shape, dtype, index: int, align: int = 16):
     """(tensor, address) of an output: the caller's, checked, or a new one."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = _empty(shape, dtype=dtype, device=_device(index))
         return t, t.data_ptr()
-    if tuple(t.shape) != tuple(shape):
+    p = _ptr(t, name, dtype, index, align)
+    if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}")
-    return t, _ptr(t, name, dtype, device, align)
+    return t, p
+
+
+_devices = {}
+
+
+def _device(index: int):
+    d = _devices.get(index)
+    if d is None:
+        d = _devices[index] = torch.device("cuda", index)
+    return d
 
 
 def rope_append(q, k, v, positions, inv_freq, k_pool, v_pool, block_table, kv_lens, cu_rows, *,
@@ -133,21 +175,20 @@ def rope_append(q, k, v, positions, inv_freq, k_pool, v_pool, block_table, kv_le
     of each of the R/2 pairs (default: all 0).  kv_lens counts the rows: the i-th
     of a session's n rows goes to cached token kv_len - n + i.
     """
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+    index = _index(k_pool)
+    if not isinstance(q, _Tensor) or q.dim() != 3:
         raise ValueError("q must be [rows][Hq][D]")
-    rows, Hq = q.shape[0], q.shape[1]
-    b = _sessions(k_pool, block_table, kv_lens, cu_rows, rows, Hq)
-    if cu_rows is None:
-        raise ValueError("cu_rows is needed")
-    dev, D, Hkv = k_pool.device, b.head_dim, b.num_kv_heads
-    qp, qs = _rows_ptr(q, "q", Hq, rows, D, dev)
-    kp, ks = _rows_ptr(k, "k", Hkv, rows, D, dev)
-    vp, vs = _rows_ptr(v, "v", Hkv, rows, D, dev)
-    pos = _ptr(positions, "positions", _I32, dev, 4)
-    if positions.dim() not in (1, 2) or positions.shape[-1] != rows:
+    rows, Hq, _ = q.shape
+    b = _sessions(k_pool, block_table, kv_lens, cu_rows, rows, Hq, index)
+    D, Hkv = b.head_dim, b.num_kv_heads
+    qp, qs = _rows_ptr(q, "q", Hq, rows, D, index)
+    kp, ks = _rows_ptr(k, "k", Hkv, rows, D, index)
+    vp, vs = _rows_ptr(v, "v", Hkv, rows, D, index)
+    pos = _ptr(positions, "positions", _I32, index, 4)
+    ps = positions.shape
+    if len(ps) not in (1, 2) or ps[-1] != rows:
         raise ValueError("positions must be [rows] or [n_axes][rows]")
-    n_axes = 1 if positions.dim() == 1 else positions.shape[0]
-    inv = _ptr(inv_freq, "inv_freq", _F64, dev, 8)
+    inv = _ptr(inv_freq, "inv_freq", _F64, index, 8)
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be [R / 2]")
     pairs = inv_freq.shape[0]
@@ -155,11 +196,11 @@ def rope_append(q, k, v, positions, inv_freq, k_pool, v_pool, block_table, kv_le
         axes = bytes(axes)
         if len(axes) != pairs:
             raise ValueError("axes must name the axis of each of inv_freq's pairs")
-    pools = _pools(k_pool, v_pool)
-    rope = PaRope(2 * pairs, n_axes, 1 if interleaved else 0, axes, pos, inv)
-    with _Call(dev, stream) as cs:
-        q_out, op = _out(q_out, "q_out", (rows, Hq, D), _BF16, dev)
-        _check(lib().pa_rope_append(ctypes.byref(b), ctypes.byref(rope), qp, qs, kp, ks, vp, vs, *pools, op, cs),
+    kpool, vpool = _ptr(k_pool, "k_pool", _BF16, index), _v_ptr(v_pool, k_pool, index)
+    rope = PaRope(2 * pairs, 1 if len(ps) == 1 else ps[0], 1 if interleaved else 0, axes, pos, inv)
+    with _on(index, stream):
+        q_out, op = _out(q_out, "q_out", (rows, Hq, D), _BF16, index)
+        _check(lib().pa_rope_append(_ref(b), _ref(rope), qp, qs, kp, ks, vp, vs, kpool, vpool, op, _current(index)),
                "pa_rope_append")
     return q_out
 
@@ -168,23 +209,38 @@ def window_workspace(q, k_pool, block_table, kv_lens, cu_rows, *, window: int = 
     """A workspace for window_attend calls of these shapes (pa_window_workspace_size):
     one serves any number of calls in stream order, calls that may overlap on the
     GPU need one each."""
-    b = _sessions(k_pool, block_table, kv_lens, cu_rows, q.shape[0], q.shape[1])
-    return _workspace(b, window, sinks, k_pool.device)
+    index = _index(k_pool)
+    _q_ptr(q, k_pool, index)
+    b = _sessions(k_pool, block_table, kv_lens, cu_rows, q.shape[0], q.shape[1], index)
+    return _empty(_workspace_bytes(b, window, sinks, index), dtype=torch.uint8, device=_device(index))
 
 
-def _workspace(b: PaSessions, window: int, sinks: int, device):
-    n = ctypes.c_size_t()
-    _check(lib().pa_window_workspace_size(ctypes.byref(b), window, sinks, ctypes.byref(n)), "pa_window_workspace_size")
-    return torch.empty(n.value, dtype=torch.uint8, device=device)
+_sizes = {}
+
+
+def _workspace_bytes(b: PaSessions, window: int, sinks: int, index: int) -> int:
+    """pa_window_workspace_size, which depends on the sizes of a call only."""
+    key = (b.n_sessions, b.num_rows, b.num_q_heads, b.num_kv_heads, b.head_dim, b.page_size, b.max_pages,
+           b.num_pages_in_pool, window, sinks, index)
+    size = _sizes.get(key)
+    if size is None:
+        n = ctypes.c_size_t()
+        with _on(index, None):
+            _check(lib().pa_window_workspace_size(_ref(b), window, sinks, _ref(n)), "pa_window_workspace_size")
+        if len(_sizes) >= 1024:
+            _sizes.clear()
+        size = _sizes[key] = n.value
+    return size
 
 
 def window_status(workspace, stream=None) -> int:
     """The device status word of the last window_attend on this workspace
     (pa_window_status; PA_OK unless a bounded wait gave up).  Synchronises the stream."""
     out = ctypes.c_int()
-    wp = _ptr(workspace, "workspace", torch.uint8, workspace.device, 256)
-    with _Call(workspace.device, stream) as cs:
-        _check(lib().pa_window_status(wp, cs, ctypes.byref(out)), "pa_window_status")
+    index = workspace.get_device()
+    wp = _ptr(workspace, "workspace", torch.uint8, index, 256)
+    with _on(index, stream):
+        _check(lib().pa_window_status(wp, _current(index), _ref(out)), "pa_window_status")
     return out.value
 
 
@@ -198,21 +254,19 @@ def window_attend(q, k_pool, v_pool, block_table, kv_lens, cu_rows, *, window: i
     [rows][Hq][D], lse fp32 [rows][Hq]); rows that see nothing get 0 and -inf.
     `workspace` (window_workspace) is allocated by the call when not given.
     """
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be [rows][Hq][D]")
-    rows, Hq = q.shape[0], q.shape[1]
-    b = _sessions(k_pool, block_table, kv_lens, cu_rows, rows, Hq)
-    dev, D = k_pool.device, b.head_dim
-    qp = _q(q, D, dev)
-    pools = _pools(k_pool, v_pool)
-    with _Call(dev, stream) as cs:
-        out, op = _out(out, "out", (rows, Hq, D), _BF16, dev)
-        lse, lp = _out(lse, "lse", (rows, Hq), _F32, dev, 4)
+    index = _index(k_pool)
+    qp = _q_ptr(q, k_pool, index)
+    rows, Hq, D = q.shape
+    b = _sessions(k_pool, block_table, kv_lens, cu_rows, rows, Hq, index)
+    kp, vp = _ptr(k_pool, "k_pool", _BF16, index), _v_ptr(v_pool, k_pool, index)
+    with _on(index, stream):
+        out, op = _out(out, "out", (rows, Hq, D), _BF16, index)
+        lse, lp = _out(lse, "lse", (rows, Hq), _F32, index, 4)
         if workspace is None:
-            workspace = _workspace(b, window, sinks, dev)
-        wp = _ptr(workspace, "workspace", torch.uint8, dev, 256)
-        _check(lib().pa_window_attend(ctypes.byref(b), window, sinks, softmax_scale, qp, *pools, wp, workspace.numel(),
-                                      op, lp, cs), "pa_window_attend")
+            workspace = _empty(_workspace_bytes(b, window, sinks, index), dtype=torch.uint8, device=_device(index))
+        wp = _ptr(workspace, "workspace", torch.uint8, index, 256)
+        _check(lib().pa_window_attend(_ref(b), window, sinks, softmax_scale, qp, kp, vp, wp, workspace.numel(), op, lp,
+                                      _current(index)), "pa_window_attend")
     return out, lse
 
 
@@ -221,20 +275,19 @@ def weigh_tokens(q, k_pool, lse, block_table, kv_lens, cu_rows, scores, *, windo
     """Adds to scores fp32 [S][Hkv][max_tokens], in place, the attention weight that
     each cached token draws from the batch's rows (pa_weigh_tokens): lse is
     window_attend's for the same q, window, sinks and scale.  Returns scores."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be [rows][Hq][D]")
-    rows, Hq = q.shape[0], q.shape[1]
-    b = _sessions(k_pool, block_table, kv_lens, cu_rows, rows, Hq)
-    dev = k_pool.device
-    qp, kp = _q(q, b.head_dim, dev), _ptr(k_pool, "k_pool", _BF16, dev)
-    lp = _ptr(lse, "lse", _F32, dev, 4)
-    if tuple(lse.shape) != (rows, Hq):
+    index = _index(k_pool)
+    qp, kp = _q_ptr(q, k_pool, index), _ptr(k_pool, "k_pool", _BF16, index)
+    rows, Hq, _ = q.shape
+    b = _sessions(k_pool, block_table, kv_lens, cu_rows, rows, Hq, index)
+    lp = _ptr(lse, "lse", _F32, index, 4)
+    if lse.shape != (rows, Hq):
         raise ValueError("lse must be [rows][Hq]")
-    sp = _ptr(scores, "scores", _F32, dev, 4)
-    if scores.dim() != 3 or scores.shape[0] != b.n_sessions or scores.shape[1] != b.num_kv_heads:
+    sp = _ptr(scores, "scores", _F32, index, 4)
+    ss = scores.shape
+    if len(ss) != 3 or ss[0] != b.n_sessions or ss[1] != b.num_kv_heads:
         raise ValueError("scores must be [S][Hkv][max_tokens]")
-    with _Call(dev, stream) as cs:
-        _check(lib().pa_weigh_tokens(ctypes.byref(b), window, sinks, softmax_scale, qp, kp, lp, sp, scores.shape[2], cs),
+    with _on(index, stream):
+        _check(lib().pa_weigh_tokens(_ref(b), window, sinks, softmax_scale, qp, kp, lp, sp, ss[2], _current(index)),
                "pa_weigh_tokens")
     return scores
 
@@ -243,9 +296,9 @@ def weigh_status(device=None, stream=None) -> int:
     """The first failure of a bounded wait of weigh_tokens on the device since this
     call last returned one (pa_weigh_status; PA_OK: none).  Synchronises the stream."""
     out = ctypes.c_int()
-    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    with _Call(device, stream) as cs:
-        _check(lib().pa_weigh_status(cs, ctypes.byref(out)), "pa_weigh_status")
+    index = torch.cuda.current_device() if device is None else torch.device(device).index or 0
+    with _on(index, stream):
+        _check(lib().pa_weigh_status(_current(index), _ref(out)), "pa_weigh_status")
     return out.value
 
 
@@ -256,21 +309,24 @@ def evict_tokens(scores, k_pool, v_pool, block_table, kv_lens, dst_table, budget
     order to the pages of dst_table int32 [S][n] (pa_evict_tokens; pages that no
     row of block_table names).  Returns (new_lens int32 [S], kept int32
     [S][Hkv][budget] former indices then -1, scores_out fp32 [S][Hkv][max_tokens])."""
-    b = _sessions(k_pool, block_table, kv_lens, None, 0, None)
-    dev, S, Hkv = k_pool.device, b.n_sessions, b.num_kv_heads
-    pools = _pools(k_pool, v_pool)
-    sp = _ptr(scores, "scores", _F32, dev, 4)
-    if scores.dim() != 3 or scores.shape[0] != S or scores.shape[1] != Hkv:
+    index = _index(k_pool)
+    b = _sessions(k_pool, block_table, kv_lens, None, 0, None, index)
+    S, Hkv = b.n_sessions, b.num_kv_heads
+    kp, vp = _ptr(k_pool, "k_pool", _BF16, index), _v_ptr(v_pool, k_pool, index)
+    sp = _ptr(scores, "scores", _F32, index, 4)
+    ss = scores.shape
+    if len(ss) != 3 or ss[0] != S or ss[1] != Hkv:
         raise ValueError("scores must be [S][Hkv][max_tokens]")
-    dp = _ptr(dst_table, "dst_table", _I32, dev, 4)
-    if dst_table.dim() != 2 or dst_table.shape[0] != S:
+    dp = _ptr(dst_table, "dst_table", _I32, index, 4)
+    ds = dst_table.shape
+    if len(ds) != 2 or ds[0] != S:
         raise ValueError("dst_table must be [S][pages]")
     if budget < 1:
         raise ValueError("budget must be positive")
-    with _Call(dev, stream) as cs:
-        scores_out, xp = _out(scores_out, "scores_out", scores.shape, _F32, dev, 4)
-        kept = torch.empty((S, Hkv, budget), dtype=_I32, device=dev)
-        new_lens = torch.empty((S,), dtype=_I32, device=dev)
-        _check(lib().pa_evict_tokens(ctypes.byref(b), sp, scores.shape[2], *pools, dp, dst_table.shape[1], budget, sinks,
-                                     recent, xp, kept.data_ptr(), new_lens.data_ptr(), cs), "pa_evict_tokens")
+    with _on(index, stream):
+        scores_out, xp = _out(scores_out, "scores_out", ss, _F32, index, 4)
+        dev = _device(index)
+        kept, new_lens = _empty((S, Hkv, budget), dtype=_I32, device=dev), _empty((S,), dtype=_I32, device=dev)
+        _check(lib().pa_evict_tokens(_ref(b), sp, ss[2], kp, vp, dp, ds[1], budget, sinks, recent, xp, kept.data_ptr(),
+                                     new_lens.data_ptr(), _current(index)), "pa_evict_tokens")
     return new_lens, kept, scores_out

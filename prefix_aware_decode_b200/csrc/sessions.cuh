@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "pa.h"
@@ -84,3 +85,34 @@ inline pa::Sessions pa_device_sessions(const pa_sessions& b) {
 }
 
 inline bool pa_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// Dynamic shared memory of a kernel, allowed once per device (`done`: a bit per device).
+template <typename K>
+bool pa_allow_smem(K* kernel, int bytes, int device, std::atomic<uint64_t>& done) {
+  const uint64_t bit = device >= 0 && device < 64 ? 1ull << device : 0;
+  if (bit && (done.load(std::memory_order_relaxed) & bit)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
+
+// The current device and its SMs (148 without a device).
+struct pa_device {
+  int index = -1, sms = 148;
+};
+inline pa_device pa_current_device() {
+  static std::atomic<int> known[64];
+  pa_device d;
+  if (cudaGetDevice(&d.index) != cudaSuccess) {
+    cudaGetLastError();
+    return d;
+  }
+  const bool slot = d.index >= 0 && d.index < 64;
+  const int n = slot ? known[d.index].load(std::memory_order_relaxed) : 0;
+  if (n > 0) {
+    d.sms = n;
+  } else if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, d.index) == cudaSuccess && slot) {
+    known[d.index].store(d.sms, std::memory_order_relaxed);
+  }
+  return d;
+}

@@ -1,0 +1,89 @@
+// Device helpers of the session-cache tensor-core kernels.
+#pragma once
+
+#include "ptx.cuh"
+
+namespace pa {
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+
+// After a wait gave up the barriers no longer tell what is in flight: 5 ms are
+// far more than any copy or product of this CTA can take to land.
+__device__ __forceinline__ void settle() {
+  const uint64_t t0 = global_timer_ns();
+  while (global_timer_ns() - t0 < 5000000ull) __nanosleep(1000);
+}
+
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
+
+// A block of `np` <= 8 pages (lane from + i of the warp holds the pool row of the
+// i-th) into 128-row x 64-dim swizzled tiles, by a converged warp whose elected
+// lane issues: the rows come by shuffles, so that each copy's operands are
+// uniform (copies issued by eight lanes each took 78 cycles apiece).
+template <int HALVES>
+__device__ __forceinline__ void load_pages(uint32_t dst, const void* tmap, int row, int from, int np, uint32_t bar,
+                                           bool lead) {
+  int r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = __shfl_sync(0xffffffffu, row, from + i);
+  if (lead) {
+    mbar_arrive_expect_tx(bar, (uint32_t)np * (HALVES * 2048));
+    if (np == 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int h = 0; h < HALVES; ++h) tma_load_2d(dst + h * 16384 + i * 2048, tmap, 64 * h, r[i], bar);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < np)
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h) tma_load_2d(dst + h * 16384 + i * 2048, tmap, 64 * h, r[i], bar);
+    }
+  }
+  __syncwarp();
+}
+
+// umma_sdesc_sw128 from an address already in 16-byte units.
+__device__ __forceinline__ uint64_t sdesc_sw128_lo(uint32_t addr16, uint32_t lbo16, uint32_t sbo16) {
+  return (uint64_t)(addr16 | (lbo16 << 16)) | ((uint64_t)(sbo16 | (1u << 14) | (2u << 29)) << 32);
+}
+
+// 2^x of two finite x <= 127 on the FMA pipe: x = n + f, f in [-1/2, 1/2]; 2^f by
+// the degree-5 polynomial of least relative error (Remez exchange, 7.5e-8), n
+// added to the exponent.  x below -126 counts as -126.
+__device__ __forceinline__ float2 exp2_fma(float2 x) {
+  x.x = fmaxf(x.x, -126.f);
+  x.y = fmaxf(x.y, -126.f);
+  // adding 1.5 * 2^23 rounds to an integer, which its low bits then hold
+  const float2 t = fadd2(x, make_float2(12582912.f, 12582912.f));
+  const float2 n = fadd2(t, make_float2(-12582912.f, -12582912.f));
+  const float2 f = ffma2(n, make_float2(-1.f, -1.f), x);
+  float2 p = make_float2(1.3276472454890609e-3f, 1.3276472454890609e-3f);
+  p = ffma2(p, f, make_float2(9.675540961325169e-3f, 9.675540961325169e-3f));
+  p = ffma2(p, f, make_float2(5.550713092088699e-2f, 5.550713092088699e-2f));
+  p = ffma2(p, f, make_float2(0.24022120237350464f, 0.24022120237350464f));
+  p = ffma2(p, f, make_float2(0.6931469440460205f, 0.6931469440460205f));
+  p = ffma2(p, f, make_float2(1.0000001192092896f, 1.0000001192092896f));
+  p.x = __uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23));
+  p.y = __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23));
+  return p;
+}
+
+}  // namespace pa

@@ -534,8 +534,8 @@ pa_status launch(WeighArgs& a, const pa_sessions& b, const void* q, const void* 
   if (!tmap_q(&tq, q, b.num_rows, b.num_q_heads, D, G, 128 / G) ||
       !tmap_pool(&tk, k_pool, b.num_pages_in_pool, b.num_kv_heads, D))
     return PA_ERR_CUDA;
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const pa_device dev = pa_current_device();
+  const int sms = dev.sms;
   // The longest possible line: every session at the table's width (or its window).
   int64_t pages = b.max_pages;
   if (a.w.window) {
@@ -554,8 +554,8 @@ pa_status launch(WeighArgs& a, const pa_sessions& b, const void* q, const void* 
   if (a.nk > 8) a.nk = 8;
   a.per_group = (b.n_sessions + kGroups - 1) / kGroups;
   constexpr int smem = weigh_smem<D>();
-  if (cudaFuncSetAttribute(weigh_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return PA_ERR_CUDA;
+  static std::atomic<uint64_t> allowed{0};
+  if (!pa_allow_smem(weigh_kernel<D>, smem, dev.index, allowed)) return PA_ERR_CUDA;
   weigh_kernel<D><<<grid, kThreads, smem, cs>>>(a, tq, tk);
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

@@ -810,16 +810,15 @@ int log2_group(const pa_sessions& b) {
 }
 
 struct Launch {
-  int grid, slots, min_span;
+  int grid, slots, min_span, device;
   size_t off_desc, off_lse, off_o, bytes;
 };
 
 // At most one CTA per SM, and no more than the longest possible line of blocks fills.
 bool plan_launch(const pa_sessions& b, const Window& w, Launch* out) {
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  cudaGetLastError();
+  const pa_device dev = pa_current_device();
+  const int sms = dev.sms;
+  out->device = dev.index;
   const int T = 256 >> log2_group(b);
   const int64_t slots = (int64_t)b.num_rows / T + b.n_sessions;
   if (slots > (int64_t)kMaxChunks * kThreads) return false;
@@ -870,7 +869,8 @@ bool launch(const pa::AttendArgs& a, const pa::Launch& l, const CUtensorMap& tq,
             const CUtensorMap& tv, cudaStream_t cs) {
   auto* k = pa::window_attend_kernel<D>;
   constexpr int smem = pa::Shape<D>::SMEM;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
+  static std::atomic<uint64_t> allowed{0};
+  if (!pa_allow_smem(k, smem, l.device, allowed)) return false;
   k<<<l.grid, pa::kThreads, smem, cs>>>(a, tq, tk, tv);
   if (cudaGetLastError() != cudaSuccess) return false;
   if (l.grid == 1) return true;  // one CTA cuts no item

@@ -575,36 +575,57 @@ def test_refusals_of_single_arguments():
         assert _lib_status("pa_rope_append", *a) == bad, (i, v)
 
 
-def test_python_refuses_what_the_library_cannot_see():
+def test_there_is_no_cpu_path():
     c = Cache([20, 5], [2, 1], 8, 2, 64, device="cpu")
-    args = [c.q, c.k, c.v, c.table, c.lens, c.cu]
+    with pytest.raises(ValueError, match="CUDA"):
+        pad.window_attend(c.q, c.k, c.v, c.table, c.lens, c.cu)
+
+
+@gpu
+def test_python_refuses_what_the_library_cannot_see():
+    """Wrong types, shapes, strides and devices: every call raises before anything is enqueued."""
+    c = Cache([20, 5], [2, 1], 8, 2, 64)
+    c.q, c.k, c.v, c.table, c.cu = c.dev("q", "k", "v", "table", "cu")
+    c_lens = c.lens.cuda()
+    args = [c.q, c.k, c.v, c.table, c_lens, c.cu]
+    pad.window_attend(*args)
     for i, t in [(0, c.q.float()), (0, c.q[:, :, :32]), (1, c.k.half()), (1, c.k[0]), (2, c.v[1:]), (3, c.table.long()),
-                 (3, c.table[0]), (4, c.lens.long()), (4, c.lens[:1]), (5, c.cu[:2]), (5, c.cu.float())]:
+                 (3, c.table[0]), (4, c_lens.long()), (4, c_lens[:1]), (5, c.cu[:2]), (5, c.cu.float())]:
         a = list(args)
         a[i] = t
         with pytest.raises(ValueError):
             pad.window_attend(*a)
-    with pytest.raises(ValueError):  # no CPU path
-        pad.window_attend(*args)
-    scores = torch.zeros(2, 2, 64)
-    lse = torch.zeros(3, 8)
+    for i in range(6):  # a tensor of another device
+        a = list(args)
+        a[i] = args[i].cpu()
+        with pytest.raises(ValueError):
+            pad.window_attend(*a)
+    for kw in (dict(out=c.q[:2]), dict(out=c.q.float()), dict(lse=torch.zeros(3, 8)), dict(window=-1), dict(sinks=-1),
+               dict(softmax_scale=-1.0), dict(softmax_scale=math.inf), dict(softmax_scale=math.nan)):
+        with pytest.raises((ValueError, pad.PaError)):
+            pad.window_attend(*args, **kw)
+    small = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    with pytest.raises(pad.PaError):
+        pad.window_attend(*args, workspace=small)
+    scores = torch.zeros(2, 2, 64, device="cuda")
+    lse = torch.zeros(3, 8, device="cuda")
     for kw in (dict(scores=scores[0]), dict(scores=scores[:1]), dict(scores=scores.double()), dict(lse=lse[:2]),
                dict(scores=scores.transpose(1, 2))):
         d = dict(dict(scores=scores, lse=lse), **kw)
         with pytest.raises(ValueError):
-            pad.weigh_tokens(c.q, c.k, d["lse"], c.table, c.lens, c.cu, d["scores"])
-    for dst in (torch.zeros(3, 4).int(), torch.zeros(2, 4).long(), torch.zeros(2).int()):
+            pad.weigh_tokens(c.q, c.k, d["lse"], c.table, c_lens, c.cu, d["scores"])
+    for dst in (torch.zeros(3, 4).int().cuda(), torch.zeros(2, 4).long().cuda(), torch.zeros(2).int().cuda()):
         with pytest.raises(ValueError):
-            pad.evict_tokens(scores, c.k, c.v, c.table, c.lens, dst, 32)
+            pad.evict_tokens(scores, c.k, c.v, c.table, c_lens, dst, 32)
     with pytest.raises(ValueError):
-        pad.evict_tokens(scores, c.k, c.v, c.table, c.lens, torch.zeros(2, 4).int(), 0)
-    kv = torch.zeros(3, 2, 64).bfloat16()
-    pos, inv = torch.zeros(3).int(), torch.ones(32, dtype=torch.float64)
+        pad.evict_tokens(scores, c.k, c.v, c.table, c_lens, torch.zeros(2, 4).int().cuda(), 0)
+    kv = torch.zeros(3, 2, 64).bfloat16().cuda()
+    pos, inv = torch.zeros(3).int().cuda(), torch.ones(32, dtype=torch.float64, device="cuda")
     rope = dict(q=c.q, k=kv, v=kv, positions=pos, inv_freq=inv)
     for kw in (dict(q=c.q[:2]), dict(k=kv.float()), dict(k=kv[:, :1]), dict(positions=pos.long()), dict(positions=pos[:2]),
                dict(inv_freq=inv.float()), dict(axes=[0] * 31), dict(q=c.q.transpose(1, 2)), dict(axes=[300] * 32),
-               dict(v=torch.zeros(3, 2, 68).bfloat16()[..., :64])):
+               dict(v=torch.zeros(3, 2, 68).bfloat16().cuda()[..., :64])):
         d = dict(rope, **kw)
         with pytest.raises(ValueError):
-            pad.rope_append(d["q"], d["k"], d["v"], d["positions"], d["inv_freq"], c.k, c.v, c.table, c.lens, c.cu,
+            pad.rope_append(d["q"], d["k"], d["v"], d["positions"], d["inv_freq"], c.k, c.v, c.table, c_lens, c.cu,
                             axes=d.get("axes"))
