@@ -23,7 +23,7 @@ from ._binding import PaRope, PaSessions, _check, lib
 
 _ref = ctypes.byref
 _I32, _F32, _F64, _BF16 = torch.int32, torch.float32, torch.float64, torch.bfloat16
-_Tensor, _empty = torch.Tensor, torch.empty
+_Tensor, _empty_strided = torch.Tensor, torch.empty_strided
 
 
 def _ptr(t, name: str, dtype, index: int, align: int = 16) -> int:
@@ -146,12 +146,19 @@ def _q_ptr(q, k_pool, index: int) -> int:
 def _out(t, name: str, shape, dtype, index: int, align: int = 16):
     """(tensor, address) of an output: the caller's, checked, or a new one."""
     if t is None:
-        t = _empty(shape, dtype=dtype, device=_device(index))
+        t = _new(shape, dtype, index)
         return t, t.data_ptr()
     p = _ptr(t, name, dtype, index, align)
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}")
     return t, p
+
+
+def _new(shape, dtype, index: int):
+    """A new contiguous tensor of at most three dimensions (empty_strided costs two thirds of empty)."""
+    n = len(shape)
+    strides = (1,) if n == 1 else (shape[1], 1) if n == 2 else (shape[1] * shape[2], shape[2], 1)
+    return _empty_strided(shape, strides, dtype=dtype, device=_device(index))
 
 
 _devices = {}
@@ -212,7 +219,7 @@ def window_workspace(q, k_pool, block_table, kv_lens, cu_rows, *, window: int = 
     index = _index(k_pool)
     _q_ptr(q, k_pool, index)
     b = _sessions(k_pool, block_table, kv_lens, cu_rows, q.shape[0], q.shape[1], index)
-    return _empty(_workspace_bytes(b, window, sinks, index), dtype=torch.uint8, device=_device(index))
+    return _new((_workspace_bytes(b, window, sinks, index),), torch.uint8, index)
 
 
 _sizes = {}
@@ -263,7 +270,7 @@ def window_attend(q, k_pool, v_pool, block_table, kv_lens, cu_rows, *, window: i
         out, op = _out(out, "out", (rows, Hq, D), _BF16, index)
         lse, lp = _out(lse, "lse", (rows, Hq), _F32, index, 4)
         if workspace is None:
-            workspace = _empty(_workspace_bytes(b, window, sinks, index), dtype=torch.uint8, device=_device(index))
+            workspace = _new((_workspace_bytes(b, window, sinks, index),), torch.uint8, index)
         wp = _ptr(workspace, "workspace", torch.uint8, index, 256)
         _check(lib().pa_window_attend(_ref(b), window, sinks, softmax_scale, qp, kp, vp, wp, workspace.numel(), op, lp,
                                       _current(index)), "pa_window_attend")
@@ -325,8 +332,7 @@ def evict_tokens(scores, k_pool, v_pool, block_table, kv_lens, dst_table, budget
         raise ValueError("budget must be positive")
     with _on(index, stream):
         scores_out, xp = _out(scores_out, "scores_out", ss, _F32, index, 4)
-        dev = _device(index)
-        kept, new_lens = _empty((S, Hkv, budget), dtype=_I32, device=dev), _empty((S,), dtype=_I32, device=dev)
+        kept, new_lens = _new((S, Hkv, budget), _I32, index), _new((S,), _I32, index)
         _check(lib().pa_evict_tokens(_ref(b), sp, ss[2], kp, vp, dp, ds[1], budget, sinks, recent, xp, kept.data_ptr(),
                                      new_lens.data_ptr(), _current(index)), "pa_evict_tokens")
     return new_lens, kept, scores_out
