@@ -65,6 +65,22 @@ __device__ __forceinline__ uint64_t sdesc_sw128_lo(uint32_t addr16, uint32_t lbo
   return (uint64_t)(addr16 | (lbo16 << 16)) | ((uint64_t)(sbo16 | (1u << 14) | (2u << 29)) << 32);
 }
 
+// Whole warp: 8 fp32 columns of its 32 TMEM lanes times each lane's f.
+__device__ __forceinline__ void tmem_scale8(uint32_t taddr, float f) {
+  uint32_t r[8];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // 2^x of two finite x <= 127 on the FMA pipe: x = n + f, f in [-1/2, 1/2]; 2^f by
 // the degree-5 polynomial of least relative error (Remez exchange, 7.5e-8), n
 // added to the exponent.  x below -126 counts as -126.

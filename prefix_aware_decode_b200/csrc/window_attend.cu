@@ -42,6 +42,7 @@ constexpr int kThreads = 384;
 constexpr int kMaxChunks = 256;      // chunks of kThreads tile slots that a CTA sums
 constexpr int kQueue = 2;            // entries of the CTA's item queue
 constexpr int kParts = 2;              // parts of a block's weights that are handed over one by one
+constexpr int kWholeBlocks = 8;        // items of at most so many blocks are not cut
 constexpr float kRaise = 8.f;        // log2 growth of a maximum that raises it
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
@@ -56,6 +57,7 @@ struct AttendArgs {
   Window w;
   int lg;              // log2 G
   int slots, min_span;
+  int whole;           // items are not cut: a CTA takes those that start in its span
   float scale_log2;
   uint16_t* out;
   float* lse;
@@ -74,16 +76,27 @@ struct Tile {
   __device__ __forceinline__ int page_index(int v) const { return v < ns ? v : v + off; }
 };
 
-// Tile slots: session s owns [cu[s] / T + s, cu[s + 1] / T + s + 1), at least
-// as many as it has tiles of T tokens; the rest are empty.
-__device__ __forceinline__ int slot_begin(const Sessions& b, int s, int lt) { return (b.row_begin(s) >> lt) + s; }
+// Sessions' first rows and lengths, from the device arrays or a shared copy.
+struct FromGlobal {
+  const Sessions& b;
+  __device__ __forceinline__ int begin(int s) const { return b.row_begin(s); }
+  __device__ __forceinline__ int kv(int s) const { return b.kv_len(s); }
+};
+struct FromShared {
+  const int *cu, *len;
+  __device__ __forceinline__ int begin(int s) const { return cu[s]; }
+  __device__ __forceinline__ int kv(int s) const { return len[s]; }
+};
 
-__device__ __forceinline__ Tile make_tile(const AttendArgs& a, int slot, int s) {
+// Tile slots: session s owns [begin(s) / T + s, begin(s + 1) / T + s + 1), at
+// least as many as it has tiles of T = 2^lt tokens; the rest are empty.
+template <typename From>
+__device__ __forceinline__ Tile make_tile(const AttendArgs& a, const From& f, int slot, int s) {
   const int lt = 8 - a.lg;
   Tile t;
   t.s = s;
-  const int b0 = a.b.row_begin(s), n = a.b.row_begin(s + 1) - b0, kv = a.b.kv_len(s);
-  t.i0 = (slot - slot_begin(a.b, s, lt)) << lt;
+  const int b0 = f.begin(s), n = f.begin(s + 1) - b0, kv = f.kv(s);
+  t.i0 = (slot - ((b0 >> lt) + s)) << lt;
   t.n_tok = min(1 << lt, n - t.i0);
   t.r0 = b0 + t.i0;
   t.p0 = kv - n + t.i0;
@@ -104,11 +117,12 @@ __device__ __forceinline__ Tile make_tile(const AttendArgs& a, int slot, int s) 
 }
 
 // Session of a slot by bisection (one thread).
-__device__ __forceinline__ int find_slot_session(const Sessions& b, int slot, int lt) {
-  int lo = 0, hi = b.S;
+template <typename From>
+__device__ __forceinline__ int find_slot_session(const From& f, int S, int slot, int lt) {
+  int lo = 0, hi = S;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (slot_begin(b, mid, lt) <= slot) lo = mid;
+    if ((f.begin(mid) >> lt) + mid <= slot) lo = mid;
     else hi = mid;
   }
   return lo;
@@ -146,29 +160,19 @@ struct Misc {
 };
 static_assert(sizeof(Misc) <= 3072, "shared memory");
 
-// sums of kThreads slots' blocks, per chunk (aliases the ring before any load)
+// What a CTA finds its span with (aliases the ring before any load): sums of
+// kThreads slots' blocks, per chunk, and a copy of the sessions' rows and
+// lengths when there are at most kCopied (bisecting the device arrays costs a
+// memory round trip a step).
+constexpr int kCopied = 4096;
 struct Sums {
   long long chunk[kMaxChunks];
   long long warp[kThreads / 32];
   long long lo_rest;
   int lo_slot, pad;
+  int cu[kCopied + 1], len[kCopied];
 };
-
-// Whole warp: 8 fp32 columns of its 32 TMEM lanes times each lane's f.
-__device__ __forceinline__ void tmem_scale8(uint32_t taddr, float f) {
-  uint32_t r[8];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
+static_assert(sizeof(Sums) <= 5 * Shape<64>::TILE, "ring");
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -188,62 +192,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int lt = 8 - a.lg;
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
-
-  // ---------------- the line of blocks and this CTA's span
-  long long total = 0;
-  const int n_chunks = (a.slots + kThreads - 1) / kThreads;
-  auto slot_blocks = [&](int slot) -> long long {
-    if (slot >= a.slots) return 0;
-    const Tile t = make_tile(a, slot, find_slot_session(a.b, slot, lt));
-    return (long long)t.blocks() * a.b.Hkv;
-  };
-  for (int c = 0; c < n_chunks; ++c) {
-    long long x = slot_blocks(c * kThreads + tid);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    if (lane == 0) su.warp[warp] = x;
-    __syncthreads();
-    if (tid == 0) {
-      long long y = 0;
-      for (int w = 0; w < kThreads / 32; ++w) y += su.warp[w];
-      su.chunk[c] = y;
-    }
-    __syncthreads();
-  }
-  for (int c = 0; c < n_chunks; ++c) total += su.chunk[c];
-  const long long span = max((long long)a.min_span, (total + gridDim.x - 1) / gridDim.x);
-  const long long lo = blockIdx.x * span, hi = min(total, lo + span);
-  if (lo >= total) {
-    if (tid == 0) a.desc[blockIdx.x].first = -1;
-    if (tid == 0 && blockIdx.x == 0) *a.status = 0;
-    return;  // uniform over the CTA
-  }
-  {
-    long long before = 0;
-    int c = 0;
-    while (before + su.chunk[c] <= lo) before += su.chunk[c++];
-    // exclusive prefix inside the chunk
-    const int slot = c * kThreads + tid;
-    const long long x = slot_blocks(slot);
-    long long inc = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    __syncthreads();
-    if (lane == 31) su.warp[warp] = inc;
-    __syncthreads();
-    long long exc = before + inc - x;
-    for (int w = 0; w < warp; ++w) exc += su.warp[w];
-    if (x > 0 && exc <= lo && lo < exc + x) {
-      su.lo_slot = slot;
-      su.lo_rest = lo - exc;
-    }
-    __syncthreads();
-  }
-  const int lo_slot = su.lo_slot;
-  const long long lo_rest = su.lo_rest;
 
   if (tid == 0) {
     for (int i = 0; i < S::NS; ++i) {
@@ -268,7 +216,77 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (blockIdx.x == 0) *a.status = 0;
     fence_mbar_init();
   }
+  if (warp == 9 && lane == 0) {
+    prefetch_tmap(&tq);
+    prefetch_tmap(&tk);
+    prefetch_tmap(&tv);
+  }
+
+  // ---------------- the line of blocks and this CTA's span
+  const bool copied = a.b.S <= kCopied;
+  if (copied) {
+    for (int s = tid; s <= a.b.S; s += kThreads) {
+      su.cu[s] = a.b.row_begin(s);
+      if (s < a.b.S) su.len[s] = a.b.kv_len(s);
+    }
+    __syncthreads();
+  }
+  auto slot_blocks = [&](int slot) -> long long {
+    if (slot >= a.slots) return 0;
+    auto blocks = [&](auto f) { return make_tile(a, f, slot, find_slot_session(f, a.b.S, slot, lt)).blocks(); };
+    return (long long)(copied ? blocks(FromShared{su.cu, su.len}) : blocks(FromGlobal{a.b})) * a.b.Hkv;
+  };
+  // exclusive prefix of x over the CTA's threads, and its sum
+  auto scan = [&](long long x, long long& sum) -> long long {
+    long long inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    __syncthreads();
+    if (lane == 31) su.warp[warp] = inc;
+    __syncthreads();
+    long long before = 0;
+    sum = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w == warp) before = sum;
+      sum += su.warp[w];
+    }
+    return before + inc - x;
+  };
+  const int n_chunks = (a.slots + kThreads - 1) / kThreads;
+  long long total = 0, x = 0, exc = 0, sum = 0;
+  for (int c = 0; c < n_chunks; ++c) {
+    x = slot_blocks(c * kThreads + tid);
+    exc = scan(x, sum);
+    if (tid == 0) su.chunk[c] = sum;
+    total += sum;
+  }
+  const long long span = max((long long)a.min_span, (total + gridDim.x - 1) / gridDim.x);
+  const long long lo = blockIdx.x * span, hi = min(total, lo + span);
+  if (lo >= total) {
+    if (tid == 0) a.desc[blockIdx.x].first = -1;
+    return;  // uniform over the CTA
+  }
   if (warp == 8) tmem_alloc(smem_u32(&mi.tmem), 512);
+  {
+    int c = 0;
+    if (n_chunks > 1) {
+      __syncthreads();
+      long long before = 0;
+      while (before + su.chunk[c] <= lo) before += su.chunk[c++];
+      x = slot_blocks(c * kThreads + tid);
+      exc = before + scan(x, sum);
+    }
+    if (x > 0 && exc <= lo && lo < exc + x) {
+      su.lo_slot = c * kThreads + tid;
+      su.lo_rest = lo - exc;
+    }
+    __syncthreads();
+  }
+  const int lo_slot = su.lo_slot;
+  const long long lo_rest = su.lo_rest;
   fence_proxy_async_smem();  // the ring held the sums
   tc_fence_before();
   __syncthreads();
@@ -307,22 +325,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     // ---------------- items and loads
     const bool lead = elect_one();
-    if (lead) {
-      prefetch_tmap(&tq);
-      prefetch_tmap(&tk);
-      prefetch_tmap(&tv);
-    }
+    const FromGlobal from{a.b};
     int slot = lo_slot;
-    Tile t = make_tile(a, slot, find_slot_session(a.b, slot, lt));
+    Tile t = make_tile(a, from, slot, find_slot_session(from, a.b.S, slot, lt));
     int g = (int)(lo_rest / t.blocks()), b0 = (int)(lo_rest % t.blocks());
     long long left = hi - lo;
     int base = 0, it = 0, issued = 0, n_q = 0;
     bool ok = true;
+    auto next_item = [&]() {  // the item after (slot, g), when there is more to do
+      b0 = 0;
+      if (++g == a.b.Hkv) {
+        g = 0;
+        while (left > 0 && ++slot < a.slots) {
+          t = make_tile(a, from, slot, find_slot_session(from, a.b.S, slot, lt));
+          if (t.np > 0) break;
+        }
+      }
+    };
+    if (a.whole && b0 > 0) {  // that item is the CTA's before
+      left -= t.blocks() - b0;
+      next_item();
+    }
     const int oob = a.b.num_pages * a.b.Hkv * kPage;  // a row past the pool: zeros
     if (lane == 0) {
       Desc d{};
       d.first = -1;
-      if (b0 > 0) {
+      if (b0 > 0 && !a.whole) {
         const long long start = lo - b0, end = start + t.blocks();
         d.first = (int)(start / span);
         d.last = (int)((end - 1) / span);
@@ -335,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     while (left > 0 && ok) {
       const int nb = t.blocks();
-      const int b1 = (int)min((long long)nb, b0 + left);
+      const int b1 = a.whole ? nb : (int)min((long long)nb, b0 + left);
       const int n = b1 - b0, e = it % kQueue;
       if (it >= kQueue && !wwait(mi.it_empty[e], it / kQueue - 1, 1)) break;
       if (lane == 0) {
@@ -385,14 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       base += 2 * n;
       left -= n;
       ++it;
-      b0 = 0;
-      if (++g == a.b.Hkv) {
-        g = 0;
-        while (left > 0 && ++slot < a.slots) {
-          t = make_tile(a, slot, find_slot_session(a.b, slot, lt));
-          if (t.np > 0) break;
-        }
-      }
+      next_item();
     }
     // end of the line for the other roles
     const int e = it % kQueue;
@@ -603,7 +624,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!(ok = wwait(mi.s_full[grp], ps++, 13))) break;
         tc_fence_after();
-        if (!busy) {
+        // none of the tile's rows sees a key of the block: all weights are 0
+        const bool none = t_first > p_max || (a.w.window != 0 && v0 >= t.ns && t_last <= p_min - a.w.window &&
+                                              t_first >= a.w.sinks);
+        if (!busy || none) {
+          if (busy) {
+            float z[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z[i] = 0.f;
+            tmem_st32(t_s, z);
+            tmem_st32(t_s + 32, z);
+            tmem_wait_st();
+          }
           tc_fence_before();
           __syncwarp();
           if (lane == 0)
@@ -626,10 +658,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t from = low < 0 ? 0xffffu : 0xffffu << min(low + 1, 16);
             const uint32_t sink = sk <= 0 ? 0u : 0xffffu >> (16 - min(sk, 16));
             const uint32_t see = gone ? 0u : upto & (from | sink);
+            if (__any_sync(0xffffffffu, see != 0xffffu)) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float& y = x[pg >> 1][16 * (pg & 1) + i];
-              y = see & (1u << i) ? y : -INFINITY;
+              for (int i = 0; i < 16; ++i) {
+                float& y = x[pg >> 1][16 * (pg & 1) + i];
+                y = see & (1u << i) ? y : -INFINITY;
+              }
             }
           }
         }
@@ -769,10 +803,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 8) tmem_free(tmem, 512);
 }
 
-// Joins the partial rows of the items that the spans cut: block (c, y) takes
-// rows [8 y, 8 y + 8) of the item cut at the start of CTA c's span, when c is
-// the first cut of that item.  One warp per row; parts in the order of their
-// keys.
+// Joins the partial rows of the items that the spans cut: blocks (c, y) take the
+// item cut at the start of CTA c + 1's span, when that is the item's first cut.
+// One warp per row, every kJoinY * 8-th of them; parts in the order of their keys.
+constexpr int kJoinY = 8;
 template <int D>
 __global__ void __launch_bounds__(256) window_join_kernel(const AttendArgs a) {
   griddep_wait();
@@ -780,27 +814,29 @@ __global__ void __launch_bounds__(256) window_join_kernel(const AttendArgs a) {
   constexpr int W = D / 32;
   const Desc d = a.desc[blockIdx.x + 1];
   if (d.first != (int)blockIdx.x) return;
-  const int prow = blockIdx.y * 8 + warp;
-  const bool pair = (d.n_tok << a.lg) > 128;
-  const int tok = prow >> a.lg;  // tile 1 starts at row 128, token 128 / G
-  if (tok >= d.n_tok || (!pair && prow >= 128)) return;
-  float mx = -INFINITY;
-  for (int c = d.first; c <= d.last; ++c)
-    mx = fmaxf(mx, a.part_lse[(size_t)(c == d.first ? d.slot0 : 2 * c) * 256 + prow]);
-  float sum = 0.f, acc[W] = {};
-  for (int c = d.first; c <= d.last; ++c) {
-    const size_t at = (size_t)(c == d.first ? d.slot0 : 2 * c) * 256 + prow;
-    const float f = mx == -INFINITY ? 0.f : ex2(a.part_lse[at] - mx);
-    sum += f;
+  const int rows = d.n_tok << a.lg;  // tile 1 of a pair starts at row 128, token 128 / G
+  for (int prow = blockIdx.y * 8 + warp; prow < rows; prow += kJoinY * 8) {
+    auto slot_of = [&](int c) { return (size_t)(c == d.first ? d.slot0 : 2 * c) * 256 + prow; };
+    float mx = -INFINITY;
+    for (int c = d.first + lane; c <= d.last; c += 32) mx = fmaxf(mx, a.part_lse[slot_of(c)]);
 #pragma unroll
-    for (int i = 0; i < W; ++i) acc[i] += f * a.part_o[at * D + lane * W + i];
+    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    float sum = 0.f, acc[W] = {};
+#pragma unroll 4
+    for (int c = d.first; c <= d.last; ++c) {
+      const size_t at = slot_of(c);
+      const float f = mx == -INFINITY ? 0.f : ex2(a.part_lse[at] - mx);
+      sum += f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) acc[i] += f * a.part_o[at * D + lane * W + i];
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const size_t ro = (size_t)(d.row0 + (prow >> a.lg)) * a.b.Hq + (d.g << a.lg) + (prow & ((1 << a.lg) - 1));
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + ro * D) + lane * (W / 2);
+#pragma unroll
+    for (int i = 0; i < W; i += 2) dst[i / 2] = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+    if (a.lse && lane == 0) a.lse[ro] = sum > 0.f ? (mx + lg2(sum)) * kLn2 : -INFINITY;
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-  const size_t ro = (size_t)(d.row0 + tok) * a.b.Hq + (d.g << a.lg) + (prow & ((1 << a.lg) - 1));
-  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + ro * D) + lane * (W / 2);
-#pragma unroll
-  for (int i = 0; i < W; i += 2) dst[i / 2] = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
-  if (a.lse && lane == 0) a.lse[ro] = sum > 0.f ? (mx + lg2(sum)) * kLn2 : -INFINITY;
 }
 
 // log2 of G (1, 2, 4, 8)
@@ -810,7 +846,7 @@ int log2_group(const pa_sessions& b) {
 }
 
 struct Launch {
-  int grid, slots, min_span, device;
+  int grid, slots, min_span, whole, device;
   size_t off_desc, off_lse, off_o, bytes;
 };
 
@@ -828,6 +864,9 @@ bool plan_launch(const pa_sessions& b, const Window& w, Launch* out) {
     if (seen < pages) pages = seen;
   }
   const int64_t line = slots * b.num_kv_heads * ((pages + 7) / 8);
+  // a cut costs partial rows, a second load of Q and the join: about as much as
+  // 8 blocks, so items of no more than that stay whole
+  out->whole = (pages + 7) / 8 <= kWholeBlocks;
   out->min_span = 2;
   const int64_t most = (line + out->min_span - 1) / out->min_span;
   out->grid = (int)(most < sms ? (most < 1 ? 1 : most) : sms);
@@ -873,9 +912,9 @@ bool launch(const pa::AttendArgs& a, const pa::Launch& l, const CUtensorMap& tq,
   if (!pa_allow_smem(k, smem, l.device, allowed)) return false;
   k<<<l.grid, pa::kThreads, smem, cs>>>(a, tq, tk, tv);
   if (cudaGetLastError() != cudaSuccess) return false;
-  if (l.grid == 1) return true;  // one CTA cuts no item
+  if (l.grid == 1 || a.whole) return true;  // no item is cut
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(l.grid - 1, 32);
+  cfg.gridDim = dim3(l.grid - 1, pa::kJoinY);
   cfg.blockDim = dim3(256);
   cfg.stream = cs;
   cudaLaunchAttribute at{};
@@ -908,6 +947,7 @@ extern "C" pa_status pa_window_attend(const pa_sessions* b, int32_t window, int3
   a.lg = pa::log2_group(*b);
   a.slots = l.slots;
   a.min_span = l.min_span;
+  a.whole = l.whole;
   a.scale_log2 = (softmax_scale != 0.f ? softmax_scale : 1.f / sqrtf((float)b->head_dim)) * pa::kLog2e;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
