@@ -4,13 +4,21 @@
 // the last `recent` and, of the rest, the `quota` = budget - sinks - recent with
 // the highest scores, ties to the lowest index; all n when n <= budget.
 //
-//   select  one CTA per (session, kv head): the quota-th highest score by a
-//           radix selection (8 bits a pass over a histogram in shared memory),
-//           then one ordered pass that writes the kept indices and scores
+//   select  a cluster of CTAs per (session, kv head), each with a run of the
+//           tokens whose order-preserving keys it holds in shared memory (re-read
+//           from memory when they do not fit): the quota-th highest key by a radix
+//           selection, 11 + 11 + 10 bits, over histograms that the cluster adds up
+//           through distributed shared memory (the scores' exponents are few, so
+//           8-bit digits made lanes collide; and one copy per four warps); then
+//           every warp counts what it keeps of its run, and with the counts before
+//           it writes the kept indices and scores in order.  Up to 1024 tokens,
+//           one a thread, are ranked by comparing each with all
 //   gather  copies the kept K and V rows, in order, to the destination pages
 //
-// The selection is bound by its passes over the scores (L2 after the first),
-// the gather by memory.
+// The selection reads the scores once; the gather, which moves the bytes, is
+// bound by memory.
+#include <type_traits>
+
 #include "ptx.cuh"
 #include "sessions.cuh"
 
@@ -18,7 +26,10 @@ namespace pa {
 namespace {
 
 constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kGatherThreads = 256;
+constexpr int kKeysMax = 32768;  // keys that a CTA holds in shared memory (128 KB)
+constexpr int kBins = 2048, kCopies = 8;
 
 struct EvictArgs {
   Sessions b;
@@ -29,131 +40,312 @@ struct EvictArgs {
   int dst_max_pages, budget, sinks, recent;
   float* scores_out;
   int32_t *kept, *new_lens;
+  int held_keys;  // keys that the launch's shared memory holds per CTA (0: none)
+  int small;      // no row has more than kSelThreads tokens
 };
 
 // Order-preserving map of a score to an unsigned key: NaN above every number,
 // -0 equal to +0.
 __device__ __forceinline__ uint32_t score_key(float f) {
-  if (f != f) return 0xffffffffu;
   const uint32_t u = __float_as_uint(f + 0.f);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  const uint32_t k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+  return f != f ? 0xffffffffu : k;
+}
+
+struct SelShared {
+  int cta_count[2];  // kept outright, equal to the threshold; read by the cluster
+  int pick, rank;
+  int warp_count[2][kSelWarps];
+  int warp_sum[kSelWarps];
+};
+struct SelHist {
+  int hist[kCopies][kBins];
+  int cta_hist[2][kBins];  // by parity of the pass; read by the cluster
+};
+
+__device__ __forceinline__ unsigned cluster_rank() {
+  unsigned r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ unsigned cluster_size() {
+  unsigned r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// An int of this CTA's shared memory as CTA `rank` of the cluster has it.
+__device__ __forceinline__ int cluster_read(const int* p, unsigned rank) {
+  uint32_t at;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
+// Sum of the first n <= 32 of v, by a whole warp.
+__device__ __forceinline__ int sum_before(const int* v, int n, int lane) {
+  return __reduce_add_sync(0xffffffffu, lane < n ? v[lane] : 0);
 }
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs a) {
-  __shared__ int hist[256];
-  __shared__ int s_pick, s_rank;
-  __shared__ uint32_t wsum[32];
+  extern __shared__ __align__(16) uint8_t sel_smem[];
+  __shared__ SelShared sh;
+  uint32_t* keys = reinterpret_cast<uint32_t*>(sel_smem);
+  SelHist& hi_ = *reinterpret_cast<SelHist*>(sel_smem + 4 * a.held_keys);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int s = blockIdx.x / a.b.Hkv, g = blockIdx.x % a.b.Hkv;
-  const int64_t row = (int64_t)s * a.b.Hkv + g;
+  const int C = (int)cluster_size(), rank_c = (int)cluster_rank();
+  const int64_t row = blockIdx.x / C;
+  const int s = (int)(row / a.b.Hkv), g = (int)(row % a.b.Hkv);
   const float* x = a.scores + row * a.max_tokens;
   float* out = a.scores_out + row * a.max_tokens;
   int32_t* kept = a.kept + row * a.budget;
   const int n = (int)min((int64_t)a.b.kv_len(s), a.max_tokens);
   const int n_new = min(n, a.budget);
-  if (tid == 0 && g == 0) a.new_lens[s] = n_new;
-  // tokens past the kept ones
-  for (int64_t t = n_new + tid; t < a.max_tokens; t += kSelThreads) out[t] = 0.f;
-  for (int t = n_new + tid; t < a.budget; t += kSelThreads) kept[t] = -1;
-  if (n <= a.budget) {
-    for (int t = tid; t < n; t += kSelThreads) {
+  const int all = C * kSelThreads, me = rank_c * kSelThreads + tid;
+  if (me == 0 && g == 0) a.new_lens[s] = n_new;
+  if (n <= a.budget) {  // uniform over the cluster
+    for (int t = me; t < n; t += all) {
       out[t] = x[t];
       kept[t] = t;
     }
     return;
   }
   const int lo = a.sinks, hi = n - a.recent, quota = a.budget - a.sinks - a.recent;
-  uint32_t prefix = 0, mask = 0;
-  int rank = quota;  // the rank-th highest key among those that match the prefix
-  if (quota > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      if (tid < 256) hist[tid] = 0;
-      __syncthreads();
-      for (int t = lo + tid; t < hi; t += kSelThreads) {
-        const uint32_t key = score_key(x[t]);
-        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255], 1);
-      }
-      __syncthreads();
-      if (warp == 0) {
-        // bins from the highest down: lane l holds bins 255 - 8l .. 248 - 8l
-        int c[8], sum = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum += c[j] = hist[255 - 8 * lane - j];
-        int above = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, above, o);
-          if (lane >= o) above += y;
-        }
-        above -= sum;  // keys in higher bins than this lane's
-        if (above < rank && above + sum >= rank) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (above < rank && above + c[j] >= rank) {
-              s_pick = 255 - 8 * lane - j;
-              s_rank = rank - above;
-            }
-            above += c[j];
-          }
-        }
-      }
-      __syncthreads();
-      prefix |= (uint32_t)s_pick << shift;
-      mask |= 255u << shift;
-      rank = s_rank;
-      __syncthreads();
-    }
-  }
-  // one ordered pass: a token stays if held, above the threshold, or among the
-  // first `rank` equal to it.  Counts of both kinds in the halves of one word.
-  int base = 0, ties = 0;
-  for (int t0 = 0; t0 < n; t0 += kSelThreads) {
-    const int t = t0 + tid;
-    const float f = t < n ? x[t] : 0.f;
-    const bool held = t < n && (t < lo || t >= hi);
+  if (a.small) {  // one CTA, n <= 1024: thread t has token t
+    const bool there = tid < n, mid = there && tid >= lo && tid < hi;
+    const float f = there ? x[tid] : 0.f;
+    // a token's place in the order (key, then the lower index); keys outside the
+    // middle are 0, which is no score's key
     const uint32_t key = score_key(f);
-    const bool mid = t < n && !held && quota > 0;
-    const bool take = held || (mid && key > prefix), tie = mid && key == prefix;
-    uint32_t v = (take ? 1u : 0u) | (tie ? 0x10000u : 0u), inc = v;
+    keys[tid] = mid ? key : 0u;
+    __syncthreads();
+    int before = 0;
+    if (quota > 0 && __any_sync(0xffffffffu, mid)) {
+      const uint4* k4 = reinterpret_cast<const uint4*>(keys);
+      const int end = (n + 3) >> 2, own = warp * 8;
+      int b0 = 0, b1 = 0, b2 = 0, b3 = 0;
+#pragma unroll 4
+      for (int t = 0; t < own; ++t) {  // lower indices: ties count
+        const uint4 k = k4[t];
+        b0 += k.x >= key, b1 += k.y >= key, b2 += k.z >= key, b3 += k.w >= key;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const uint32_t k = __shfl_sync(0xffffffffu, mid ? key : 0u, i);
+        b0 += i < lane ? k >= key : k > key;
+      }
+#pragma unroll 4
+      for (int t = own + 8; t < end; ++t) {
+        const uint4 k = k4[t];
+        b0 += k.x > key, b1 += k.y > key, b2 += k.z > key, b3 += k.w > key;
+      }
+      before = b0 + b1 + b2 + b3;
+    }
+    const bool keep = there && (!mid || before < quota);
+    const unsigned m = __ballot_sync(0xffffffffu, keep);
+    if (lane == 0) sh.warp_sum[warp] = __popc(m);
+    __syncthreads();
+    int j = __popc(m & ((1u << lane) - 1));
+    j += sum_before(sh.warp_sum, warp, lane);
+    if (keep) {
+      kept[j] = tid;
+      out[j] = f;
+    }
+    return;
+  }
+  // this CTA's tokens [c0, c1), this warp's [w0, w1): multiples of 128, four a lane
+  const int seg = ((n + C - 1) / C + 127) & ~127;
+  const int c0 = min(n, rank_c * seg), c1 = min(n, c0 + seg);
+  const int wseg = ((c1 - c0 + kSelWarps - 1) / kSelWarps + 127) & ~127;
+  const int w0 = min(c1, c0 + warp * wseg), w1 = min(c1, w0 + wseg);
+  const bool held = a.held_keys > 0;
+  // Four keys of tokens t .. t + 3, 0 for those that the selection does not rank
+  // (held or past the run): below every score's key, so no rank counts them.
+  const bool vec = (a.max_tokens & 3) == 0 && (reinterpret_cast<uintptr_t>(a.scores) & 15) == 0;
+  const int m0 = max(lo, w0), m1 = min(hi, w1);  // the warp's ranked tokens
+  auto load_keys = [&](int t) -> uint4 {
+    float f[4];
+    if (vec) {
+      const float4 v = *reinterpret_cast<const float4*>(x + t);
+      f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = t + i < w1 ? x[t + i] : 0.f;
+    }
+    uint32_t k[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) k[i] = t + i >= m0 && t + i < m1 ? score_key(f[i]) : 0u;
+    return make_uint4(k[0], k[1], k[2], k[3]);
+  };
+  if (held) {
+#pragma unroll 4
+    for (int t = w0 + 4 * lane; t < w1; t += 128) *reinterpret_cast<uint4*>(keys + (t - c0)) = load_keys(t);
+  }
+  __syncwarp();
+  auto keys_at = [&](int t) { return held ? *reinterpret_cast<const uint4*>(keys + (t - c0)) : load_keys(t); };
+  uint32_t prefix = 0;
+  int rank = quota;  // the rank-th highest key among those that match the prefix
+  auto pass = [&](auto shift_tag, auto bits_tag, int parity) {
+    constexpr int shift = decltype(shift_tag)::value, bits = decltype(bits_tag)::value;
+    constexpr uint32_t digit = (1u << bits) - 1, mask = shift + bits == 32 ? 0u : ~0u << (shift + bits);
+    int* hist = hi_.hist[warp / (kSelWarps / kCopies)];
+    for (int i = tid; i < kCopies * kBins / 4; i += kSelThreads)
+      reinterpret_cast<int4*>(hi_.hist[0])[i] = make_int4(0, 0, 0, 0);
+    __syncthreads();
+    for (int t = w0 + 4 * lane; t < w1; t += 128) {
+      const uint4 k = keys_at(t);
+      const uint32_t kk[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (mask == 0 || ((kk[i] ^ prefix) & mask) == 0) atomicAdd(&hist[(kk[i] >> shift) & digit], 1);
+    }
+    __syncthreads();
+    // bins from the highest down, two a thread
+    const int b = kBins - 2 - 2 * tid;
+    int2 c = make_int2(0, 0);  // x: bin b + 1, y: bin b
+#pragma unroll
+    for (int w = 0; w < kCopies; ++w) {
+      const int2 v = *reinterpret_cast<const int2*>(&hi_.hist[w][b]);
+      c.x += v.y;
+      c.y += v.x;
+    }
+    if (C > 1) {
+      hi_.cta_hist[parity][b + 1] = c.x;
+      hi_.cta_hist[parity][b] = c.y;
+      cluster_sync();
+      c = make_int2(0, 0);
+      for (int r = 0; r < C; ++r) {
+        c.x += cluster_read(&hi_.cta_hist[parity][b + 1], r);
+        c.y += cluster_read(&hi_.cta_hist[parity][b], r);
+      }
+    }
+    int above = c.x + c.y;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, above, o);
+      if (lane >= o) above += y;
+    }
+    if (lane == 31) sh.warp_sum[warp] = above;
+    __syncthreads();
+    above += sum_before(sh.warp_sum, warp, lane) - c.x - c.y;  // keys in higher bins than this thread's
+    if (above < rank && above + c.x >= rank) {
+      sh.pick = b + 1;
+      sh.rank = rank - above;
+    } else if (above + c.x < rank && above + c.x + c.y >= rank) {
+      sh.pick = b;
+      sh.rank = rank - above - c.x;
+    }
+    __syncthreads();
+    prefix |= (uint32_t)sh.pick << shift;
+    rank = sh.rank;
+  };
+  if (quota > 0) {
+    using std::integral_constant;
+    pass(integral_constant<int, 21>{}, integral_constant<int, 11>{}, 0);
+    pass(integral_constant<int, 10>{}, integral_constant<int, 11>{}, 1);
+    pass(integral_constant<int, 0>{}, integral_constant<int, 10>{}, 0);
+  } else {
+    prefix = 0xffffffffu;  // nothing is above it, and `rank` = 0 takes no tie
+  }
+  // A token stays if held outright (sinks, recent, above the threshold) or among
+  // the first `rank` equal to it.  Four tokens of a lane: bit i of the low half:
+  // token t + i is kept outright, of the high half: it ties
+  auto kinds = [&](int t, const uint32_t(&kk)[4]) -> uint32_t {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (kk[i] > prefix) m |= 1u << i;
+      if (kk[i] == prefix) m |= 0x10000u << i;
+    }
+    if (t < lo || t + 3 >= m1) {  // not all ranked
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t + i < w1 && (t + i < lo || t + i >= hi)) m |= 1u << i;
+    }
+    return m;
+  };
+  auto counts = [](uint32_t m) { return (uint32_t)__popc(m & 0xffffu) | (uint32_t)__popc(m >> 16) << 16; };
+  // every warp counts both kinds of its run ...
+  int takes = 0, ties = 0;
+  for (int t = w0 + 4 * lane; t < w1; t += 128) {
+    const uint4 k = keys_at(t);
+    const uint32_t m = kinds(t, {k.x, k.y, k.z, k.w});
+    takes += __popc(m & 0xffffu);
+    ties += __popc(m >> 16);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    takes += __shfl_xor_sync(0xffffffffu, takes, o);
+    ties += __shfl_xor_sync(0xffffffffu, ties, o);
+  }
+  if (lane == 0) {
+    sh.warp_count[0][warp] = takes;
+    sh.warp_count[1][warp] = ties;
+  }
+  __syncthreads();
+  if (warp < 2) {
+    const int sum = sum_before(sh.warp_count[warp], kSelWarps, lane);
+    if (lane == 0) sh.cta_count[warp] = sum;
+  }
+  if (C > 1) cluster_sync();
+  // ... and adds up what lies before them
+  takes = ties = 0;
+  for (int c = 0; c < rank_c; ++c) {
+    takes += cluster_read(&sh.cta_count[0], c);
+    ties += cluster_read(&sh.cta_count[1], c);
+  }
+  takes += sum_before(sh.warp_count[0], warp, lane);
+  ties += sum_before(sh.warp_count[1], warp, lane);
+  for (int t0 = w0; t0 < w1; t0 += 128) {
+    const int t = t0 + 4 * lane;
+    const uint4 k = t < w1 ? keys_at(t) : make_uint4(0, 0, 0, 0);
+    const uint32_t kk[4] = {k.x, k.y, k.z, k.w};
+    const uint32_t m = t < w1 ? kinds(t, kk) : 0u, c = counts(m);
+    if (!__any_sync(0xffffffffu, m != 0)) continue;
+    uint32_t inc = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
-    if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    if (warp == 0) {
-      uint32_t w = wsum[lane];
+    int take_before = takes + (int)((inc - c) & 0xffffu), tie_before = ties + (int)((inc - c) >> 16);
+    if (m) {
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, w, o);
-        if (lane >= o) w += y;
+      for (int i = 0; i < 4; ++i) {
+        const bool take = m >> i & 1, tie = m >> (16 + i) & 1;
+        if (take || (tie && tie_before < rank)) {
+          const int j = take_before + min(tie_before, rank);
+          kept[j] = t + i;
+          out[j] = x[t + i];
+        }
+        take_before += take;
+        tie_before += tie;
       }
-      wsum[lane] = w;
     }
-    __syncthreads();
-    const uint32_t exc = inc - v + (warp ? wsum[warp - 1] : 0u);
-    const int tie_before = ties + (int)(exc >> 16);
-    if (take || (tie && tie_before < rank)) {
-      const int j = base + (int)(exc & 0xffffu) + min(tie_before, rank) - min(ties, rank);
-      kept[j] = t;
-      out[j] = f;
-    }
-    const uint32_t tot = wsum[31];
-    base += (int)(tot & 0xffffu) + min(ties + (int)(tot >> 16), rank) - min(ties, rank);
-    ties += (int)(tot >> 16);
-    __syncthreads();
+    inc = __shfl_sync(0xffffffffu, inc, 31);
+    takes += (int)(inc & 0xffffu);
+    ties += (int)(inc >> 16);
   }
+  if (C > 1) cluster_sync();  // no CTA leaves while another reads its counts
 }
 
 template <int D>
 __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(const EvictArgs a) {
   constexpr int V = D / 8;  // 16-byte vectors of a row
+  griddep_wait();  // the selection's results
   const int s = blockIdx.z, g = blockIdx.y;
   const int n_new = a.new_lens[s];
   const int j = blockIdx.x * (kGatherThreads / V) + threadIdx.x / V, c = threadIdx.x % V;
+  // what lies past the kept tokens, in equal parts
+  const int64_t row = (int64_t)s * a.b.Hkv + g;
+  const int64_t me = (int64_t)blockIdx.x * kGatherThreads + threadIdx.x, all = (int64_t)gridDim.x * kGatherThreads;
+  for (int64_t i = n_new + me; i < a.max_tokens; i += all) a.scores_out[row * a.max_tokens + i] = 0.f;
+  for (int64_t i = n_new + me; i < a.budget; i += all) a.kept[row * a.budget + i] = -1;
   if (j >= n_new || j / kPage >= a.dst_max_pages) return;
-  const int t = a.kept[((int64_t)s * a.b.Hkv + g) * a.budget + j];
+  const int t = a.kept[row * a.budget + j];
   const int sp = a.b.page(s, t / kPage), dp = a.dst_table[(size_t)s * a.dst_max_pages + j / kPage];
   if (sp < 0 || (unsigned)dp >= (unsigned)a.b.num_pages) return;
   const size_t from = (((size_t)sp * a.b.Hkv + g) * kPage + t % kPage) * D + 8 * c;
@@ -194,12 +386,47 @@ extern "C" pa_status pa_evict_tokens(const pa_sessions* b, const float* scores, 
   a.kept = kept;
   a.new_lens = new_lens;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  pa::evict_select_kernel<<<b->n_sessions * b->num_kv_heads, pa::kSelThreads, 0, cs>>>(a);
-  const int rows = pa::kGatherThreads / (b->head_dim / 8);
   const int64_t span = (int64_t)b->max_pages * pa::kPage;
+  // CTAs per (session, kv head): more while SMs would be idle and a CTA would
+  // still have 4096 tokens, or until the keys fit shared memory
+  const int64_t longest = span < max_tokens ? span : max_tokens;
+  const int64_t pairs = (int64_t)b->n_sessions * b->num_kv_heads;
+  const pa_device dev = pa_current_device();
+  int C = 1;
+  while (C < 8 && (longest / C > pa::kKeysMax || (pairs * C * 2 <= dev.sms && longest / (2 * C) >= 4096))) C *= 2;
+  a.small = longest <= pa::kSelThreads;
+  // (a warp's run is padded to 128 tokens)
+  const int64_t per_cta = ((longest + C - 1) / C + 127) / 128 * 128 + 128 * pa::kSelWarps;
+  constexpr int64_t most_held = pa::kKeysMax + 128 * pa::kSelWarps;
+  a.held_keys = a.small ? pa::kSelThreads : (int)(per_cta <= most_held ? per_cta : 0);
+  const int smem = 4 * a.held_keys + (a.small ? 0 : (int)sizeof(pa::SelHist));
+  static std::atomic<uint64_t> allowed{0};
+  if (!pa_allow_smem(pa::evict_select_kernel, 4 * (int)most_held + (int)sizeof(pa::SelHist), dev.index, allowed))
+    return PA_ERR_CUDA;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(pairs * C));
+  cfg.blockDim = dim3(pa::kSelThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = cs;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = C;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, pa::evict_select_kernel, a) != cudaSuccess) return PA_ERR_CUDA;
+  const int rows = pa::kGatherThreads / (b->head_dim / 8);
   const int most = (int)(span < budget ? span : budget);
-  const dim3 grid((most + rows - 1) / rows, b->num_kv_heads, b->n_sessions);
-  if (b->head_dim == 64) pa::evict_gather_kernel<64><<<grid, pa::kGatherThreads, 0, cs>>>(a);
-  else pa::evict_gather_kernel<128><<<grid, pa::kGatherThreads, 0, cs>>>(a);
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  cudaLaunchConfig_t cg{};
+  cg.gridDim = dim3((most + rows - 1) / rows, b->num_kv_heads, b->n_sessions);
+  cg.blockDim = dim3(pa::kGatherThreads);
+  cg.stream = cs;
+  cudaLaunchAttribute ag{};
+  ag.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  ag.val.programmaticStreamSerializationAllowed = 1;
+  cg.attrs = &ag;
+  cg.numAttrs = 1;
+  const cudaError_t e = b->head_dim == 64 ? cudaLaunchKernelEx(&cg, pa::evict_gather_kernel<64>, a)
+                                          : cudaLaunchKernelEx(&cg, pa::evict_gather_kernel<128>, a);
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

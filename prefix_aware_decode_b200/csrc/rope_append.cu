@@ -28,7 +28,30 @@ struct RopeArgs {
   uint32_t axes[4];  // 2 bits per pair: its axis
 };
 
-// ROWS consecutive rows per CTA.
+// Turns the 8 pairs of a unit: with `split` element i of the vectors is pair i,
+// else the elements 2i, 2i + 1 are.
+__device__ __forceinline__ void turn_unit(uint4& x0, uint4& x1, const float2* cs, bool split) {
+  uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const float2 p = bf16x2_to_f2(w0[m]), y = bf16x2_to_f2(w1[m]);
+    if (split) {
+      const float2 t0 = cs[2 * m], t1 = cs[2 * m + 1];
+      w0[m] = pack_bf16x2(p.x * t0.x - y.x * t0.y, p.y * t1.x - y.y * t1.y);
+      w1[m] = pack_bf16x2(p.x * t0.y + y.x * t0.x, p.y * t1.y + y.y * t1.x);
+    } else {
+      const float2 t0 = cs[m], t1 = cs[4 + m];
+      w0[m] = pack_bf16x2(p.x * t0.x - p.y * t0.y, p.x * t0.y + p.y * t0.x);
+      w1[m] = pack_bf16x2(y.x * t1.x - y.y * t1.y, y.x * t1.y + y.y * t1.x);
+    }
+  }
+  x0 = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+  x1 = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+}
+
+// ROWS consecutive rows per CTA: one while that leaves SMs idle (the fewest
+// dependent steps), four when there are enough (each thread then has six
+// vectors in flight).
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArgs a) {
   __shared__ float2 turn[ROWS][D / 2];  // (cos, sin)
@@ -68,51 +91,52 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
     }
   }
   __syncthreads();
-  // units of 16 elements (two 16-byte vectors) of a head
-  constexpr int U = D / 16;
-  const int Hq = a.b.Hq, Hkv = a.b.Hkv, rot = a.R / 16;
-  const int per_row = (Hq + 2 * Hkv) * U;
-  for (int i = tid; i < ROWS * per_row; i += kRopeThreads) {
-    const int j = i / per_row, x = i - j * per_row, h = x / U, u = x % U, r = r0 + j;
-    if (r >= a.b.rows || !live[j]) continue;
-    const uint16_t* src;
-    uint16_t* dst;
-    const bool is_v = h >= Hq + Hkv;
-    if (h < Hq) {
-      src = a.q + (int64_t)r * a.q_stride + h * D;
-      dst = a.q_out + ((int64_t)r * Hq + h) * D;
-    } else {
-      if (slot[j] < 0) continue;
-      const int g = is_v ? h - Hq - Hkv : h - Hq;
-      src = (is_v ? a.v + (int64_t)r * a.v_stride : a.k + (int64_t)r * a.k_stride) + g * D;
-      dst = (is_v ? a.v_pool : a.k_pool) + slot[j] + (int64_t)g * kPage * D;
-    }
-    // element offsets of the unit's two vectors
-    const bool split = u < rot && !a.interleaved;
-    const int e0 = split ? 8 * u : 16 * u, e1 = split ? e0 + a.R / 2 : e0 + 8;
-    uint4 x0 = *reinterpret_cast<const uint4*>(src + e0), x1 = *reinterpret_cast<const uint4*>(src + e1);
-    if (u < rot && !is_v) {
-      uint32_t w0[4] = {x0.x, x0.y, x0.z, x0.w}, w1[4] = {x1.x, x1.y, x1.z, x1.w};
-      const float2* cs = &turn[j][8 * u];
+  // Units of 16 elements (two 16-byte vectors) of a head: a thread keeps its unit
+  // u of the heads and walks the (row, head) pairs, kBatch of them with their
+  // loads in flight together.
+  constexpr int U = D / 16, STEP = kRopeThreads / U;
+  constexpr int kBatch = 2;
+  const int Hq = a.b.Hq, Hkv = a.b.Hkv, H = Hq + 2 * Hkv;
+  const int u = tid % U;
+  const bool rot = u < a.R / 16, split = rot && !a.interleaved;
+  const int e0 = split ? 8 * u : 16 * u, e1 = split ? e0 + a.R / 2 : e0 + 8;  // the unit's two vectors
+  int j = 0, h = tid / U;
+  while (h >= H) h -= H, ++j;
+  while (j < ROWS) {
+    uint4 x0[kBatch], x1[kBatch];
+    uint16_t* dst[kBatch];
+    int row[kBatch];  // the turns to apply; -1: copy
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        if (split) {  // pairs (e0 + 2m, e1 + 2m), (e0 + 2m + 1, e1 + 2m + 1)
-          const float2 p = bf16x2_to_f2(w0[m]), y = bf16x2_to_f2(w1[m]);
-          const float2 t0 = cs[2 * m], t1 = cs[2 * m + 1];
-          w0[m] = pack_bf16x2(p.x * t0.x - y.x * t0.y, p.y * t1.x - y.y * t1.y);
-          w1[m] = pack_bf16x2(p.x * t0.y + y.x * t0.x, p.y * t1.y + y.y * t1.x);
-        } else {  // each word is a pair
-          const float2 p = bf16x2_to_f2(w0[m]), y = bf16x2_to_f2(w1[m]);
-          const float2 t0 = cs[m], t1 = cs[4 + m];
-          w0[m] = pack_bf16x2(p.x * t0.x - p.y * t0.y, p.x * t0.y + p.y * t0.x);
-          w1[m] = pack_bf16x2(y.x * t1.x - y.y * t1.y, y.x * t1.y + y.y * t1.x);
+    for (int k = 0; k < kBatch; ++k) {
+      dst[k] = nullptr;
+      if (j < ROWS && r0 + j < a.b.rows && live[j]) {
+        const int64_t r = r0 + j;
+        const uint16_t* src = nullptr;
+        row[k] = rot && h < Hq + Hkv ? j : -1;
+        if (h < Hq) {
+          src = a.q + r * a.q_stride + h * D;
+          dst[k] = a.q_out + (r * Hq + h) * D;
+        } else if (slot[j] >= 0) {
+          const bool is_v = h >= Hq + Hkv;
+          const int g = is_v ? h - Hq - Hkv : h - Hq;
+          src = (is_v ? a.v + r * a.v_stride : a.k + r * a.k_stride) + g * D;
+          dst[k] = (is_v ? a.v_pool : a.k_pool) + slot[j] + (int64_t)g * kPage * D;
+        }
+        if (src) {
+          x0[k] = *reinterpret_cast<const uint4*>(src + e0);
+          x1[k] = *reinterpret_cast<const uint4*>(src + e1);
         }
       }
-      x0 = make_uint4(w0[0], w0[1], w0[2], w0[3]);
-      x1 = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+      h += STEP;
+      while (h >= H) h -= H, ++j;
     }
-    *reinterpret_cast<uint4*>(dst + e0) = x0;
-    *reinterpret_cast<uint4*>(dst + e1) = x1;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (!dst[k]) continue;
+      if (row[k] >= 0) turn_unit(x0[k], x1[k], &turn[row[k]][8 * u], split);
+      *reinterpret_cast<uint4*>(dst[k] + e0) = x0[k];
+      *reinterpret_cast<uint4*>(dst[k] + e1) = x1[k];
+    }
   }
 }
 
@@ -156,7 +180,14 @@ extern "C" pa_status pa_rope_append(const pa_sessions* b, const pa_rope* rope, c
   if (rope->axes)
     for (int i = 0; i < rope->rotary_dim / 2; ++i) a.axes[i >> 4] |= (uint32_t)rope->axes[i] << (2 * (i & 15));
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (b->head_dim == 64) pa::rope_append_kernel<64, 1><<<b->num_rows, pa::kRopeThreads, 0, cs>>>(a);
-  else pa::rope_append_kernel<128, 1><<<b->num_rows, pa::kRopeThreads, 0, cs>>>(a);
+  const bool many = b->num_rows >= 16 * pa_current_device().sms;
+  const unsigned grid = many ? (b->num_rows + 3) / 4 : b->num_rows;
+  if (b->head_dim == 64) {
+    if (many) pa::rope_append_kernel<64, 4><<<grid, pa::kRopeThreads, 0, cs>>>(a);
+    else pa::rope_append_kernel<64, 1><<<grid, pa::kRopeThreads, 0, cs>>>(a);
+  } else {
+    if (many) pa::rope_append_kernel<128, 4><<<grid, pa::kRopeThreads, 0, cs>>>(a);
+    else pa::rope_append_kernel<128, 1><<<grid, pa::kRopeThreads, 0, cs>>>(a);
+  }
   return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

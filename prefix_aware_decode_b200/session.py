@@ -111,25 +111,31 @@ class SessionPool:
             left -= take
         return runs
 
-    def compact(self, sid: int, max_tokens: int) -> List[int]:
-        """Cuts session `sid` to at most max_tokens tokens, on pages of its own:
-        the bookkeeping of an eviction (evict_tokens), which copies the kept
-        tokens to the pages returned here, from those that `tables` gave before.
-        The old pages are released (a fork keeps the ones it shares), so what
-        next takes them must be ordered after that copy.  A pool without enough
-        free pages raises MemoryError and changes nothing."""
+    def compact(self, sessions, max_tokens: int) -> List[List[int]]:
+        """Cuts every session of `sessions` to at most max_tokens tokens, on new
+        pages of its own: the bookkeeping of an eviction (evict_tokens), which
+        copies the kept tokens to the pages returned here, one list per session,
+        from those that `tables` gave before.  All new pages are taken before any
+        old one is released, so no session's copy is written over pages that
+        another's is read from; what next takes the old pages (a fork keeps those it
+        shares) must be ordered after the copies.  A pool without enough free pages
+        raises MemoryError and changes nothing."""
         if max_tokens < 1:
             raise ValueError("max_tokens must be positive")
-        s = self._sessions[sid]
-        n = min(s.n_tokens, int(max_tokens))
-        need = -(-n // self.P)
-        if need > len(self._free):
+        sids = list(sessions)
+        if len(set(sids)) != len(sids):
+            raise ValueError("a session is named twice")
+        lens = [min(self._sessions[sid].n_tokens, int(max_tokens)) for sid in sids]
+        need = [-(-n // self.P) for n in lens]
+        if sum(need) > len(self._free):
             raise MemoryError("KV pool has no free page")
-        new = [self._take() for _ in range(need)]
-        for p in s.pages:
-            self._drop(p)
-        s.pages, s.n_tokens = new, n
-        return list(new)
+        new = [[self._take() for _ in range(k)] for k in need]
+        for sid, pages, n in zip(sids, new, lens):
+            s = self._sessions[sid]
+            for p in s.pages:
+                self._drop(p)
+            s.pages, s.n_tokens = pages, n
+        return [list(p) for p in new]
 
     def close(self, sid: int):
         s = self._sessions.pop(sid)

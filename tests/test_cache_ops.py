@@ -299,6 +299,10 @@ def test_evict_ties_and_odd_scores():
 @gpu
 def test_evict_long_and_short_score_rows():
     _evict_case([70001], 1, 64, 3000, 4, 100, seed=35)
+    _evict_case([9001, 12000], 2, 64, 8000, 0, 1, seed=38)  # several CTAs a row
+    g = torch.Generator().manual_seed(6)
+    x = torch.randint(0, 3, (1, 1, 400000), generator=g).float()  # more keys than shared memory holds
+    _evict_case([345678], 1, 64, 1000, 4, 100, scores=x, seed=39)
     _evict_case([400, 90], 2, 64, 100, 4, 10, seed=36, T=257)  # lengths taken as at most max_tokens
 
 
@@ -444,7 +448,7 @@ def test_a_session_lives_through_append_attend_weigh_and_evict():
     step([5, 40])
     table, lens = pool.tables(sids)
     assert float((scores.double().cpu() - total).abs().max()) < 1e-3
-    new = [pool.compact(s, budget) for s in sids]
+    new = pool.compact(sids, budget)
     dst = torch.tensor([n + [-1] * (budget // P - len(n)) for n in new], dtype=torch.int32).cuda()
     before = scores.cpu()
     lens2, kept, scores2 = pad.evict_tokens(scores, kp, vp, torch.from_numpy(table).cuda(), torch.from_numpy(lens).cuda(),
@@ -483,19 +487,34 @@ def test_session_pool_tables_and_compact():
     assert lens.tolist() == [100, 100] and table.shape == (2, 7) and table.dtype == lens.dtype == "int32"
     assert table[0, :6].tolist() == table[1, :6].tolist() and table[0, 6] != table[1, 6]
     old = pool.pages(1)
-    new = pool.compact(1, 40)
+    new, = pool.compact([1], 40)
     assert len(new) == 3 and not set(new) & set(old) and pool.pages(1) == new and pool.tokens(1) == 40
     assert pool.pages(2)[:6] == old[:6]  # the fork keeps the shared pages
     pool.check()
-    assert pool.compact(1, 64) == pool.pages(1) and pool.tokens(1) == 40  # no more tokens than the session has
+    assert pool.compact([1], 64) == [pool.pages(1)] and pool.tokens(1) == 40  # no more tokens than the session has
     pool.check()
-    with pytest.raises(ValueError):
-        pool.compact(1, 0)
+    for bad in (([1], 0), ([1, 1], 40)):
+        with pytest.raises(ValueError):
+            pool.compact(*bad)
     pool.append(1, 16 * pool.free_pages)
     before = pool.pages(1)
     with pytest.raises(MemoryError):
-        pool.compact(1, 40)
+        pool.compact([1], 40)
     assert pool.pages(1) == before
+    pool.check()
+
+
+def test_compacted_sessions_take_no_page_that_one_of_them_held():
+    # one eviction call copies them all: a page written for one is not read for another
+    pool = SessionPool(40)
+    for s in range(4):
+        pool.open(s)
+        pool.append(s, 70 + 9 * s)
+    old = {p for s in range(4) for p in pool.pages(s)}
+    new = pool.compact([2, 0, 3, 1], 48)
+    assert [len(p) for p in new] == [3, 3, 3, 3] and len({p for n in new for p in n}) == 12
+    assert not old & {p for n in new for p in n}
+    assert [pool.pages(s) for s in (2, 0, 3, 1)] == new
     pool.check()
 
 
