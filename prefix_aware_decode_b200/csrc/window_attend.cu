@@ -610,8 +610,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int t0 = t.page_index(v0 + lane) * kPage;
           dead = t0 + kPage > kv_end || (t0 + kPage > a.w.sinks && t0 < seen_from);
         }
+        if (!(ok = wwait(mi.s_full[grp], ps++, 13))) break;
+        tc_fence_after();
         if (__any_sync(0xffffffffu, dead) && (grp == 0 || !pair)) {
           const int pv = pos_v(base, j, n);
+          // (after the block's scores: the slot's last use is then over, which the
+          // parity of a phase alone would not tell)
           if (!(ok = wwait(mi.full[pv % S::NS], pv / S::NS, 14))) break;
           const int key = tid & 127, tk0 = t.page_index(v0 + (key >> 4)) * kPage + (key & 15);
           if ((key >> 4) < pages && (tk0 >= kv_end || (tk0 >= a.w.sinks && tk0 < seen_from))) {
@@ -622,8 +626,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async_smem();
         }
-        if (!(ok = wwait(mi.s_full[grp], ps++, 13))) break;
-        tc_fence_after();
         // none of the tile's rows sees a key of the block: all weights are 0
         const bool none = t_first > p_max || (a.w.window != 0 && v0 >= t.ns && t_last <= p_min - a.w.window &&
                                               t_first >= a.w.sinks);

@@ -118,6 +118,23 @@ def test_attend_runs_alike_on_another_stream_and_twice(batch):
 
 
 @gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window,sinks,lo,hi,rows", [(700, 21, 900, 6000, 1), (0, 0, 500, 5000, 7), (300, 5, 400, 3000, 40)])
+def test_attend_many_items_a_cta(window, sinks, lo, hi, rows, D):
+    """Many short items in a row on every SM, whose blocks end inside pages: every run gives the same bits."""
+    g = torch.Generator().manual_seed(13)
+    kv = torch.randint(lo, hi, (48,), generator=g).tolist()
+    c = Cache(kv, [1 + int(i) % rows for i in torch.randint(0, 99, (48,), generator=g)], 8, 8, D, seed=14)
+    out, lse = ref.run_attend(c, window, sinks)
+    o, l, tol, ltol = ref.attend(c, window, sinks)
+    ref.check(out, o, tol, "out")
+    ref.check(lse, l, ltol, "lse")
+    for _ in range(8):
+        again, lse2 = ref.run_attend(c, window, sinks)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@gpu
 def test_attend_agrees_with_the_planned_decode():
     # one row of every session, no window: what Plan / attend compute
     c = Cache([400, 33, 1000, 16], [1, 1, 1, 1], 8, 2, 128, seed=11)
