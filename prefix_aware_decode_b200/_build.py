@@ -1,4 +1,5 @@
-"""Build libpa.so (planner + sm_100a kernels + C ABI) in the package directory.
+"""Build libpa.so (planner + sm_100a kernels + C ABI) and _cache_ops.so (the
+session-cache operators on torch tensors, over libpa.so) in the package directory.
 
 nvcc compiles every CUDA source for sm_100a only (-gencode
 arch=compute_100a,code=sm_100a) with -lineinfo; the host planner is C++17.
@@ -18,6 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(REPO, "include")
 BUILD = os.path.join(REPO, "_build")
 LIB = os.path.join(HERE, "libpa.so")
+TORCH_OPS = os.path.join(HERE, "_cache_ops.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CU_SOURCES = ["kernels.cu", "capi.cu", "noalloc.cu", "rope_append.cu", "window_attend.cu", "weigh.cu", "evict.cu"]
@@ -62,7 +64,33 @@ def build(force: bool = False, verbose: bool = False) -> str:
         tmp = LIB + ".tmp"
         subprocess.check_call([cc] + ARCH + ["-shared", "-o", tmp] + objs)
         os.replace(tmp, LIB)
+    build_torch_ops(force, verbose)
     return LIB
+
+
+def build_torch_ops(force: bool = False, verbose: bool = False) -> str:
+    """The Python module _cache_ops (csrc/torch_ops.cpp), against the installed
+    torch; libpa.so is found beside it ($ORIGIN)."""
+    src = os.path.join(CSRC, "torch_ops.cpp")
+    if not (force or _newer(TORCH_OPS, [src, os.path.join(INCLUDE, "pa.h")])):
+        return TORCH_OPS
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    tmp = TORCH_OPS + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
+           "-I", INCLUDE, "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", "/usr/local/cuda/include", "-isystem", sysconfig.get_paths()["include"], src, "-o", tmp,
+           "-L", HERE, "-lpa", "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.check_call(cmd)
+    os.replace(tmp, TORCH_OPS)
+    return TORCH_OPS
 
 
 if __name__ == "__main__":
