@@ -20,9 +20,10 @@
 // scores in 512 tensor cycles; so a part of them is computed on the FMA pipe
 // (kFmaPairs), which leaves both pipes about equally busy.
 //
-// Roles (576 threads): warps 0-15 four groups of one thread per key, each with
+// Roles (608 threads): warps 0-15 four groups of one thread per key, each with
 // its own score buffer in tensor memory; warp 16 issues the products; warp 17
-// walks the items and loads.
+// walks the items and loads the Q tiles and an item's first K block, warp 18 its
+// second (one warp took 3300 cycles to issue the copies of both).
 #include <type_traits>
 
 #include "ptx.cuh"
@@ -34,7 +35,7 @@ namespace pa {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kThreads = 576;
+constexpr int kThreads = 608;
 constexpr int kGroups = 1024;  // entries of the table of item prefixes
 constexpr int kQueue = 4;      // entries of the CTA's item queue
 constexpr int kFmaPairs = 4;   // of the 16 pairs of scores of a 32-column chunk: exponentials on the FMA pipe
@@ -48,7 +49,7 @@ struct WeighArgs {
   Window w;
   int lg;                 // log2 G
   int per_group;          // sessions per entry of the prefix table
-  int nk, nq;             // ring slots of K blocks and of Q tiles
+  int nk, nq;             // ring slots of first (and of second) K blocks, and of Q tiles
   int run;                // 1: contiguous runs of items, 0: every gridDim.x-th item
   int pair;               // key blocks of an item: 2, or 1
   const float* lse;
@@ -94,12 +95,12 @@ struct Shape {
   static constexpr int HALVES = D / 64;
   static constexpr int BLK = 128 * 128;      // 128 rows x 64 dims
   static constexpr int TILE = HALVES * BLK;  // a K block, a Q tile
-  static constexpr int SLOTS = D == 128 ? 6 : 10;
+  static constexpr int SLOTS = D == 128 ? 6 : 10;  // nk <= 8, nq <= 8
   static constexpr int OFF_MISC = SLOTS * TILE;
 };
 
 struct Misc {
-  uint64_t kfull[8], kempty[8], qfull[8], qempty[8], sfull[4], sempty[4], done;
+  uint64_t kfull[2][8], kempty[2][8], qfull[8], qempty[8], sfull[4], sempty[4], done;
   uint64_t it_full[kQueue], it_empty[kQueue], comb[kQueue];
   uint32_t tmem;
   int fail;
@@ -169,8 +170,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     mi.prefix[groups] = run;
     for (int i = 0; i < 8; ++i) {
-      mbar_init(bar(mi.kfull[i]), 1);
-      mbar_init(bar(mi.kempty[i]), 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(bar(mi.kfull[b][i]), 1);
+        mbar_init(bar(mi.kempty[b][i]), 1);
+      }
       mbar_init(bar(mi.qfull[i]), 2);               // the tile's bytes; the lse
       mbar_init(bar(mi.qempty[i]), 17);  // products; the warps that read the lse
     }
@@ -180,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kQueue; ++i) {
       mbar_init(bar(mi.it_full[i]), 1);
-      mbar_init(bar(mi.it_empty[i]), 17);
+      mbar_init(bar(mi.it_empty[i]), 18);
       mbar_init(bar(mi.comb[i]), 16);
     }
     mbar_init(bar(mi.done), 1);
@@ -210,9 +213,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return true;
   };
-  // K slots first, then Q slots
-  auto k_tile = [&](int slot) { return smem + slot * S::TILE; };
-  auto q_tile = [&](int slot) { return smem + (a.nk + slot) * S::TILE; };
+  // K slots first (a ring for each block of an item, so that each is filled by one
+  // warp that sees all of its phases), then Q slots
+  auto k_at = [&](int b, int slot) { return b * a.nk + slot; };
+  auto q_at = [&](int slot) { return a.pair * a.nk + slot; };
+  auto tile_at = [&](int at) { return smem + at * S::TILE; };
 
   if (warp == 17) {
     // ---------------- items and loads
@@ -286,19 +291,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(bar(mi.it_full[e]));
       }
       ++it;
-      // ---- K blocks: lane l has the item's l-th page
-      auto page_of = [&](int v) -> int { return lane < step && v < x.np ? a.b.page(s, x.page_index(v)) : -1; };
+      // ---- the first K block: lane l has its l-th page
+      auto page_of = [&](int v) -> int { return lane < 8 && v < x.np ? a.b.page(s, x.page_index(v)) : -1; };
       const int pg = same ? pg_next : page_of(v0 + lane);
       if (a.run && blk + 1 < nblk) pg_next = page_of(v0 + step + lane);
       const int row = pg < 0 ? oob : (pg * a.b.Hkv + g) * kPage;
-      for (int b = 0; b < a.pair && v0 + 8 * b < x.np; ++b) {
-        const int np = min(8, x.np - v0 - 8 * b);
-        if (kr.phase > 0 && !(ok = wwait(mi.kempty[kr.slot], kr.phase - 1, 2))) break;
-        load_pages<S::HALVES>(smem_u32(k_tile(kr.slot)), &tk, row, 8 * b, np, bar(mi.kfull[kr.slot]), lead);
-        ++n_k;
-        kr.next(a.nk);
-      }
-      if (!ok) break;
+      if (kr.phase > 0 && !(ok = wwait(mi.kempty[0][kr.slot], kr.phase - 1, 2))) break;
+      load_pages<S::HALVES>(smem_u32(tile_at(k_at(0, kr.slot))), &tk, row, 0, min(8, x.np - v0),
+                            bar(mi.kfull[0][kr.slot]), lead);
+      kr.next(a.nk);
+      ++n_k;
       // ---- Q tiles and their lse
       if (q_new) {
         for (int rt = one ? 0 : rt0; rt < (one ? 1 : rt1); ++rt) {
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive_expect_tx(fb, S::TILE);
 #pragma unroll
             for (int h = 0; h < S::HALVES; ++h)
-              tma_load_3d(smem_u32(q_tile(qr.slot) + h * S::BLK), &tq, 64 * h, g << a.lg, x.r0 + tok, fb);
+              tma_load_3d(smem_u32(tile_at(q_at(qr.slot)) + h * S::BLK), &tq, 64 * h, g << a.lg, x.r0 + tok, fb);
           }
           ++n_q;
 #pragma unroll
@@ -336,15 +338,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // loads in flight land before the CTA ends (all have, unless a wait gave up)
-    for (int i = max(0, n_k - a.nk); i < n_k; ++i) mbar_wait_bounded(bar(mi.kfull[i % a.nk]), (i / a.nk) & 1, kTimeoutNs);
+    for (int i = max(0, n_k - a.nk); i < n_k; ++i) mbar_wait_bounded(bar(mi.kfull[0][i % a.nk]), (i / a.nk) & 1, kTimeoutNs);
     for (int i = max(0, n_q - a.nq); i < n_q; ++i) mbar_wait_bounded(bar(mi.qfull[i % a.nq]), (i / a.nq) & 1, kTimeoutNs);
+  } else if (warp == 18) {
+    // ---------------- the items' second K blocks
+    const bool lead = elect_one();
+    const int oob = a.b.num_pages * a.b.Hkv * kPage;
+    Ring kr;
+    int n_k = 0;
+    for (int it = 0;; ++it) {
+      const int e = it % kQueue;
+      if (!wwait(mi.it_full[e], it / kQueue, 13)) break;
+      const Item& im = mi.items[e];
+      const Span x = im.x;
+      const int s = im.s, g = im.g, v0 = im.v0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(mi.it_empty[e]));
+      if (v0 < 0) break;
+      if (a.pair < 2 || v0 + 8 >= x.np) continue;
+      const int v = v0 + 8 + lane;
+      const int pg = lane < 8 && v < x.np ? a.b.page(s, x.page_index(v)) : -1;
+      const int row = pg < 0 ? oob : (pg * a.b.Hkv + g) * kPage;
+      if (kr.phase > 0 && !wwait(mi.kempty[1][kr.slot], kr.phase - 1, 14)) break;
+      load_pages<S::HALVES>(smem_u32(tile_at(k_at(1, kr.slot))), &tk, row, 0, min(8, x.np - v0 - 8),
+                            bar(mi.kfull[1][kr.slot]), lead);
+      kr.next(a.nk);
+      ++n_k;
+    }
+    for (int i = max(0, n_k - a.nk); i < n_k; ++i) mbar_wait_bounded(bar(mi.kfull[1][i % a.nk]), (i / a.nk) & 1, kTimeoutNs);
   } else if (warp == 16) {
     // ---------------- products (the whole warp walks, one elected lane issues)
     auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
     const uint32_t tm = (uint32_t)uni((int)tmem), lo = (uint32_t)uni((int)(smem_u32(smem) >> 4));
     const bool lead = elect_one();
     int it = 0, seq = 0, uses[4] = {0, 0, 0, 0};  // uses: products into each score buffer
-    Ring kr, qr, qcur;
+    Ring kr[2], qr, qcur;
     bool ok = true;
     auto commit = [&](uint64_t& b) {
       if (lead) umma_commit(bar(b));
@@ -360,12 +388,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(bar(mi.it_empty[e]));
       if (v0 < 0) break;
       const int nb = a.pair == 2 && v0 + 8 < np ? 2 : 1;
-      int kslot[2];
-      for (int b = 0; b < nb && ok; ++b) {
-        kslot[b] = kr.slot;
-        ok = wwait(mi.kfull[kr.slot], kr.phase, 6);
-        kr.next(a.nk);
-      }
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        if (b < nb && ok) ok = wwait(mi.kfull[b][kr[b].slot], kr[b].phase, 6);
       for (int rt = rt0; rt < rt1 && ok; ++rt, ++seq) {
         if (q_new) {
           qcur = qr;
@@ -383,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 4; ++i) u = i == buf ? uses[i]++ : u;
           if (u > 0 && !(ok = wwait(mi.sempty[buf], u - 1, 8))) continue;
           tc_fence_after();
-          const uint32_t ka = lo + kslot[b] * (S::TILE >> 4), qa = lo + (a.nk + qcur.slot) * (S::TILE >> 4);
+          const uint32_t ka = lo + k_at(b, kr[b].slot) * (S::TILE >> 4), qa = lo + q_at(qcur.slot) * (S::TILE >> 4);
           if (lead) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
@@ -397,7 +422,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok && q_last) commit(mi.qempty[qcur.slot]);
       }
-      for (int b = 0; b < nb && ok; ++b) commit(mi.kempty[kslot[b]]);
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        if (b < nb && ok) {
+          commit(mi.kempty[b][kr[b].slot]);
+          kr[b].next(a.nk);
+        }
       ++it;
     }
     commit(mi.done);  // every product has completed before the tensor memory is released
@@ -549,9 +579,8 @@ pa_status launch(WeighArgs& a, const pa_sessions& b, const void* q, const void* 
   const int grid = (int)(line < sms ? line : sms);
   // few rows: K streams (runs of items, the Q tile stays); many: Q streams
   a.run = (int64_t)b.num_rows * G <= (int64_t)128 * b.n_sessions;
-  a.nq = a.run ? 2 : Shape<D>::SLOTS / 2;
-  a.nk = Shape<D>::SLOTS - a.nq;
-  if (a.nk > 8) a.nk = 8;
+  a.nq = a.run ? 2 : Shape<D>::SLOTS - 2;
+  a.nk = (Shape<D>::SLOTS - a.nq) / a.pair;
   a.per_group = (b.n_sessions + kGroups - 1) / kGroups;
   constexpr int smem = weigh_smem<D>();
   static std::atomic<uint64_t> allowed{0};

@@ -15,10 +15,11 @@
 // so in both forms two softmax groups alternate and the tensor cores always
 // have a product to run while a group works on its scores.
 //
-// Schedule.  All items' blocks form one line, cut into equal spans, one per CTA
-// (one CTA per SM): every SM gets the same work whatever the lengths.  Lengths
-// live on the device, so every CTA sums the items' blocks itself to find its
-// span.  An item cut by a span's end leaves normalised partial rows (o, lse) in
+// Schedule.  The kv heads are dealt to `lanes` (up to 4); a lane's items' blocks form
+// a line, cut into equal spans, one per CTA (one CTA per SM): every SM gets the
+// same work whatever the lengths, and the CTAs of the lanes walk the same pages
+// side by side (a page holds its heads one behind the other).  Lengths live on the device, so every CTA sums the items'
+// blocks itself to find its span.  An item cut by a span's end leaves normalised partial rows (o, lse) in
 // the workspace, at most two a CTA, joined by a short second launch.
 //
 // Roles (384 threads): warps 0-3 and 4-7 softmax groups, one thread per row;
@@ -43,11 +44,12 @@ constexpr int kMaxChunks = 256;      // chunks of kThreads tile slots that a CTA
 constexpr int kQueue = 2;            // entries of the CTA's item queue
 constexpr int kParts = 2;              // parts of a block's weights that are handed over one by one
 constexpr int kWholeBlocks = 8;        // items of at most so many blocks are not cut
+constexpr int kLanes = 4;              // most kv heads walked side by side (148 SMs = 37 spans of 4)
 constexpr float kRaise = 8.f;        // log2 growth of a maximum that raises it
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 struct Desc {  // a partial item at the head of a CTA's span
-  int first, last;  // CTAs that share the item
+  int first, last;  // spans that share the item
   int slot0;        // partial slot of the first
   int row0, n_tok, g, pad0, pad1;
 };
@@ -56,7 +58,7 @@ struct AttendArgs {
   Sessions b;
   Window w;
   int lg;              // log2 G
-  int slots, min_span;
+  int slots, min_span, lanes;
   int whole;           // items are not cut: a CTA takes those that start in its span
   float scale_log2;
   uint16_t* out;
@@ -223,6 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // ---------------- the line of blocks and this CTA's span
+  const int heads = a.b.Hkv / a.lanes, in_lane = blockIdx.x % a.lanes;  // head k of the lane is k lanes + in_lane
   const bool copied = a.b.S <= kCopied;
   if (copied) {
     for (int s = tid; s <= a.b.S; s += kThreads) {
@@ -234,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto slot_blocks = [&](int slot) -> long long {
     if (slot >= a.slots) return 0;
     auto blocks = [&](auto f) { return make_tile(a, f, slot, find_slot_session(f, a.b.S, slot, lt)).blocks(); };
-    return (long long)(copied ? blocks(FromShared{su.cu, su.len}) : blocks(FromGlobal{a.b})) * a.b.Hkv;
+    return (long long)(copied ? blocks(FromShared{su.cu, su.len}) : blocks(FromGlobal{a.b})) * heads;
   };
   // exclusive prefix of x over the CTA's threads, and its sum
   auto scan = [&](long long x, long long& sum) -> long long {
@@ -263,8 +266,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) su.chunk[c] = sum;
     total += sum;
   }
-  const long long span = max((long long)a.min_span, (total + gridDim.x - 1) / gridDim.x);
-  const long long lo = blockIdx.x * span, hi = min(total, lo + span);
+  const int spans = gridDim.x / a.lanes, mine = blockIdx.x / a.lanes;
+  const long long span = max((long long)a.min_span, (total + spans - 1) / spans);
+  const long long lo = mine * span, hi = min(total, lo + span);
   if (lo >= total) {
     if (tid == 0) a.desc[blockIdx.x].first = -1;
     return;  // uniform over the CTA
@@ -328,19 +332,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const FromGlobal from{a.b};
     int slot = lo_slot;
     Tile t = make_tile(a, from, slot, find_slot_session(from, a.b.S, slot, lt));
-    int g = (int)(lo_rest / t.blocks()), b0 = (int)(lo_rest % t.blocks());
+    int b0 = (int)(lo_rest % t.blocks()), head = (int)(lo_rest / t.blocks()), g = head * a.lanes + in_lane;
     long long left = hi - lo;
     int base = 0, it = 0, issued = 0, n_q = 0;
     bool ok = true;
-    auto next_item = [&]() {  // the item after (slot, g), when there is more to do
+    auto next_item = [&]() {  // when there is more to do
       b0 = 0;
-      if (++g == a.b.Hkv) {
-        g = 0;
+      if (++head == heads) {
+        head = 0;
         while (left > 0 && ++slot < a.slots) {
           t = make_tile(a, from, slot, find_slot_session(from, a.b.S, slot, lt));
           if (t.np > 0) break;
         }
       }
+      g = head * a.lanes + in_lane;
     };
     if (a.whole && b0 > 0) {  // that item is the CTA's before
       left -= t.blocks() - b0;
@@ -354,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long start = lo - b0, end = start + t.blocks();
         d.first = (int)(start / span);
         d.last = (int)((end - 1) / span);
-        d.slot0 = start == d.first * span ? 2 * d.first : 2 * d.first + 1;
+        d.slot0 = 2 * (d.first * a.lanes + in_lane) + (start == d.first * span ? 0 : 1);
         d.row0 = t.r0;
         d.n_tok = t.n_tok;
         d.g = g;
@@ -716,8 +721,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // ---------------- the item's end
-      const int mine = pair ? n : (n - grp + 1) >> 1;  // blocks of this group
-      if (mine > 0 && !(ok = wwait(mi.o_full[grp], po++, 15))) break;
+      const int n_mine = pair ? n : (n - grp + 1) >> 1;  // blocks of this group
+      if (n_mine > 0 && !(ok = wwait(mi.o_full[grp], po++, 15))) break;
       tc_fence_after();
       float w0 = l > 0.f ? 1.f / l : 0.f, w1 = 0.f, lse2 = l > 0.f ? m + lg2(l) : -INFINITY;
       int d0 = 0, dn = D;  // dims this thread writes
@@ -745,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         src1 = tmem + S::T_O + (grp ^ 1) * D + lane_off;
         two = n > 1;
       }
-      const bool have = mine > 0;  // this group's accumulator was written
+      const bool have = n_mine > 0;  // this group's accumulator was written
       const bool live = tok < t.n_tok;
       const int r = t.r0 + tok, h = (g << a.lg) + (row & ((1 << a.lg) - 1));
       const int prow = (pair ? grp * 128 : 0) + row;
@@ -806,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the partial rows of the items that the spans cut: blocks (c, y) take the
-// item cut at the start of CTA c + 1's span, when that is the item's first cut.
+// item cut at the start of the span after CTA c's, when that is its first cut.
 // One warp per row, every kJoinY * 8-th of them; parts in the order of their keys.
 constexpr int kJoinY = 8;
 template <int D>
@@ -814,11 +819,12 @@ __global__ void __launch_bounds__(256) window_join_kernel(const AttendArgs a) {
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int W = D / 32;
-  const Desc d = a.desc[blockIdx.x + 1];
-  if (d.first != (int)blockIdx.x) return;
+  const Desc d = a.desc[blockIdx.x + a.lanes];
+  if (d.first != (int)blockIdx.x / a.lanes) return;
+  const int in_lane = blockIdx.x % a.lanes;
   const int rows = d.n_tok << a.lg;  // tile 1 of a pair starts at row 128, token 128 / G
   for (int prow = blockIdx.y * 8 + warp; prow < rows; prow += kJoinY * 8) {
-    auto slot_of = [&](int c) { return (size_t)(c == d.first ? d.slot0 : 2 * c) * 256 + prow; };
+    auto slot_of = [&](int c) { return (size_t)(c == d.first ? d.slot0 : 2 * (c * a.lanes + in_lane)) * 256 + prow; };
     float mx = -INFINITY;
     for (int c = d.first + lane; c <= d.last; c += 32) mx = fmaxf(mx, a.part_lse[slot_of(c)]);
 #pragma unroll
@@ -848,7 +854,7 @@ int log2_group(const pa_sessions& b) {
 }
 
 struct Launch {
-  int grid, slots, min_span, whole, device;
+  int grid, slots, min_span, lanes, whole, device;
   size_t off_desc, off_lse, off_o, bytes;
 };
 
@@ -865,13 +871,18 @@ bool plan_launch(const pa_sessions& b, const Window& w, Launch* out) {
     const int64_t seen = ((int64_t)w.window + T + kPage - 2) / kPage + 1 + ((int64_t)w.sinks + kPage - 1) / kPage + 1;
     if (seen < pages) pages = seen;
   }
-  const int64_t line = slots * b.num_kv_heads * ((pages + 7) / 8);
   // a cut costs partial rows, a second load of Q and the join: about as much as
   // 8 blocks, so items of no more than that stay whole
   out->whole = (pages + 7) / 8 <= kWholeBlocks;
   out->min_span = 2;
-  const int64_t most = (line + out->min_span - 1) / out->min_span;
-  out->grid = (int)(most < sms ? (most < 1 ? 1 : most) : sms);
+  out->lanes = b.num_kv_heads < kLanes ? b.num_kv_heads : kLanes;
+  while (b.num_kv_heads % out->lanes) --out->lanes;
+  const int64_t line = slots * (b.num_kv_heads / out->lanes) * ((pages + 7) / 8);
+  int64_t spans = (line + out->min_span - 1) / out->min_span;
+  const int64_t most = sms / out->lanes > 1 ? sms / out->lanes : 1;
+  if (spans > most) spans = most;
+  if (spans < 1) spans = 1;
+  out->grid = (int)spans * out->lanes;
   out->slots = (int)slots;
   out->off_desc = 256;
   out->off_lse = out->off_desc + ((size_t)out->grid * sizeof(Desc) + 255) / 256 * 256;
@@ -914,9 +925,9 @@ bool launch(const pa::AttendArgs& a, const pa::Launch& l, const CUtensorMap& tq,
   if (!pa_allow_smem(k, smem, l.device, allowed)) return false;
   k<<<l.grid, pa::kThreads, smem, cs>>>(a, tq, tk, tv);
   if (cudaGetLastError() != cudaSuccess) return false;
-  if (l.grid == 1 || a.whole) return true;  // no item is cut
+  if (l.grid == l.lanes || a.whole) return true;  // no item is cut
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(l.grid - 1, pa::kJoinY);
+  cfg.gridDim = dim3(l.grid - l.lanes, pa::kJoinY);
   cfg.blockDim = dim3(256);
   cfg.stream = cs;
   cudaLaunchAttribute at{};
@@ -950,6 +961,7 @@ extern "C" pa_status pa_window_attend(const pa_sessions* b, int32_t window, int3
   a.slots = l.slots;
   a.min_span = l.min_span;
   a.whole = l.whole;
+  a.lanes = l.lanes;
   a.scale_log2 = (softmax_scale != 0.f ? softmax_scale : 1.f / sqrtf((float)b->head_dim)) * pa::kLog2e;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
