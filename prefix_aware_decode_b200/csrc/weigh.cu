@@ -38,7 +38,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kThreads = 608;
 constexpr int kGroups = 1024;  // entries of the table of item prefixes
 constexpr int kQueue = 4;      // entries of the CTA's item queue
-constexpr int kFmaPairs = 4;   // of the 16 pairs of scores of a 32-column chunk: exponentials on the FMA pipe
+constexpr int kFmaPairs = 4;   // of 16 pairs of scores: exponentials on the FMA pipe
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 // First failure of a device-side wait since pa_weigh_status last read it.
@@ -123,6 +123,11 @@ struct Ring {
   __device__ __forceinline__ void next(int n) {
     if (++slot == n) slot = 0, ++phase;
   }
+  __device__ __forceinline__ void skip(int k, int n) {
+    slot += k;
+    phase += slot / n;
+    slot %= n;
+  }
 };
 
 template <int D>
@@ -175,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(bar(mi.kempty[b][i]), 1);
       }
       mbar_init(bar(mi.qfull[i]), 2);               // the tile's bytes; the lse
-      mbar_init(bar(mi.qempty[i]), 17);  // products; the warps that read the lse
+      mbar_init(bar(mi.qempty[i]), a.run ? 17 : 1 + 4 * a.pair);  // products; the warps that read the lse
     }
     for (int i = 0; i < 4; ++i) {
       mbar_init(bar(mi.sfull[i]), 1);
@@ -468,70 +473,85 @@ __global__ void __launch_bounds__(kThreads, 1)
         hole = a.b.page(im.s, t / kPage) < 0;
       }
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      for (int rt = rt0; rt < rt1 && ok; ++rt, ++seq) {
-        if (q_new) {
+      // one column tile, in Q slot q
+      auto tile = [&](int rt, const Ring& q) -> bool {
+        const int tok = rt << lt, cols = min(128, (n - tok) << a.lg);
+        // every key of the block sees every column
+        const bool all = cols == 128 && v1 - v0 == 8 && p0 + tok >= t_last &&
+                         (a.w.window == 0 || (v0 >= x.ns && p0 + tok + (128 >> a.lg) - 1 < (long long)t_first + a.w.window) ||
+                          t_last < a.w.sinks);
+        if (!wwait(mi.sfull[buf], uses++, 10)) return false;
+        tc_fence_after();
+        // the columns [cl, cr) of the tile see the key
+        const int cl = min(max(i0 - tok, 0), 1 << lt) << a.lg, cr = min(max(i1 - tok, 0), 1 << lt) << a.lg;
+        const float* nl = mi.nlse[q.slot];
+        const float2 sc = make_float2(a.scale_log2, a.scale_log2);
+        auto chunk = [&](auto all_tag, float(&y)[32], int c) {
+          constexpr bool ALL = decltype(all_tag)::value;
+          uint32_t see = 0xffffffffu;  // bit i: column 32 c + i sees the key
+          if (!ALL) {
+            const int l0 = min(max(cl - 32 * c, 0), 32);
+            const int l1 = min(max(cr - 32 * c, 0), 32);
+            see = l1 > l0 ? (0xffffffffu >> (32 - (l1 - l0))) << l0 : 0u;
+          }
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            const float4 l4 = *reinterpret_cast<const float4*>(nl + 32 * c + i);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float2 z = ffma2(make_float2(y[i + 2 * k], y[i + 2 * k + 1]), sc,
+                               k == 0 ? make_float2(l4.x, l4.y) : make_float2(l4.z, l4.w));
+              if (!ALL) {
+                z.x = see >> (i + 2 * k) & 1 ? z.x : -INFINITY;
+                z.y = see >> (i + 2 * k + 1) & 1 ? z.y : -INFINITY;
+              }
+              const int pr = (i >> 1) + k;
+              const bool fma = ALL && (pr * kFmaPairs) / 16 != ((pr + 1) * kFmaPairs) / 16;
+              sum[k] = fadd2(sum[k], fma ? exp2_fma(z) : make_float2(ex2(z.x), ex2(z.y)));
+            }
+          }
+        };
+        auto sweep = [&](auto all_tag) {
+          const int nc = (cols + 31) >> 5;
+#pragma unroll 1
+          for (int c = 0; c < nc; ++c) {
+            float y[32];
+            tmem_ld32(t_s + 32 * c, y);
+            tmem_wait_ld_into(y);
+            chunk(all_tag, y, c);
+          }
+        };
+        if (all) sweep(std::true_type{});
+        else sweep(std::false_type{});
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(mi.sempty[buf]));
+        return true;
+      };
+      // In a run every warp waits for every tile, its turn or not, and arrives when
+      // the slot is given back, so that its arrival belongs to this use of the slot.
+      // Else every tile is loaded anew, and a group takes the slots of its turn,
+      // always the same ones (the ring's size is a multiple of the turns).
+      const int skip = a.run ? 0 : (mine - seq) & (of - 1);
+      if (!a.run) {
+        qcur = qr;
+        qcur.skip(skip, a.nq);
+      }
+      for (int rt = rt0 + skip; rt < rt1; rt += a.run ? 1 : of) {
+        if (a.run && q_new) {
           qcur = qr;
           qr.next(a.nq);
         }
-        // every warp waits for the tile, its turn or not: its arrival on qempty below
-        // then belongs to this use of the slot (a warp that ran ahead would arrive
-        // for a later one)
         if (!(ok = wwait(mi.qfull[qcur.slot], qcur.phase, 11))) break;
-        if (seq % of == mine && there) {
-          const int tok = rt << lt, cols = min(128, (n - tok) << a.lg);
-          // every key of the block sees every column
-          const bool all = cols == 128 && v1 - v0 == 8 && p0 + tok >= t_last &&
-                           (a.w.window == 0 || (v0 >= x.ns && p0 + tok + (128 >> a.lg) - 1 < (long long)t_first + a.w.window) ||
-                            t_last < a.w.sinks);
-          if (!(ok = wwait(mi.sfull[buf], uses++, 10))) break;
-          tc_fence_after();
-          // the columns [cl, cr) of the tile see the key
-          const int cl = min(max(i0 - tok, 0), 1 << lt) << a.lg, cr = min(max(i1 - tok, 0), 1 << lt) << a.lg;
-          const float* nl = mi.nlse[qcur.slot];
-          const float2 sc = make_float2(a.scale_log2, a.scale_log2);
-          auto chunk = [&](auto all_tag, float(&y)[32], int c) {
-            constexpr bool ALL = decltype(all_tag)::value;
-            uint32_t see = 0xffffffffu;  // bit i: column 32 c + i sees the key
-            if (!ALL) {
-              const int l0 = min(max(cl - 32 * c, 0), 32);
-              const int l1 = min(max(cr - 32 * c, 0), 32);
-              see = l1 > l0 ? (0xffffffffu >> (32 - (l1 - l0))) << l0 : 0u;
-            }
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 l4 = *reinterpret_cast<const float4*>(nl + 32 * c + i);
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                float2 z = ffma2(make_float2(y[i + 2 * k], y[i + 2 * k + 1]), sc,
-                                 k == 0 ? make_float2(l4.x, l4.y) : make_float2(l4.z, l4.w));
-                if (!ALL) {
-                  z.x = see >> (i + 2 * k) & 1 ? z.x : -INFINITY;
-                  z.y = see >> (i + 2 * k + 1) & 1 ? z.y : -INFINITY;
-                }
-                const int pr = (i >> 1) + k;
-                const bool fma = ALL && (pr * kFmaPairs) / 16 != ((pr + 1) * kFmaPairs) / 16;
-                sum[k] = fadd2(sum[k], fma ? exp2_fma(z) : make_float2(ex2(z.x), ex2(z.y)));
-              }
-            }
-          };
-          auto tile = [&](auto all_tag) {
-            const int nc = (cols + 31) >> 5;
-#pragma unroll 1
-            for (int c = 0; c < nc; ++c) {
-              float y[32];
-              tmem_ld32(t_s + 32 * c, y);
-              tmem_wait_ld_into(y);
-              chunk(all_tag, y, c);
-            }
-          };
-          if (all) tile(std::true_type{});
-          else tile(std::false_type{});
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(mi.sempty[buf]));
-        }
+        if (there && (!a.run || seq % of == mine) && !(ok = tile(rt, qcur))) break;
         __syncwarp();
-        if (q_last && lane == 0) mbar_arrive(bar(mi.qempty[qcur.slot]));
+        if (lane == 0 && (!a.run || q_last)) mbar_arrive(bar(mi.qempty[qcur.slot]));
+        if (a.run) ++seq;
+        else qcur.skip(of, a.nq);
+      }
+      if (!a.run) {
+        qr.skip(rt1 - rt0, a.nq);
+        seq += rt1 - rt0;
       }
       if (!ok) break;
       // ---------------- the item's end: the groups of a block join their sums
@@ -579,7 +599,7 @@ pa_status launch(WeighArgs& a, const pa_sessions& b, const void* q, const void* 
   const int grid = (int)(line < sms ? line : sms);
   // few rows: K streams (runs of items, the Q tile stays); many: Q streams
   a.run = (int64_t)b.num_rows * G <= (int64_t)128 * b.n_sessions;
-  a.nq = a.run ? 2 : Shape<D>::SLOTS - 2;
+  a.nq = a.run ? 2 : Shape<D>::SLOTS - 2;  // 4 or 8 when not a.run: a multiple of the groups' turns
   a.nk = (Shape<D>::SLOTS - a.nq) / a.pair;
   a.per_group = (b.n_sessions + kGroups - 1) / kGroups;
   constexpr int smem = weigh_smem<D>();
