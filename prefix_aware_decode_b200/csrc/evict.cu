@@ -52,6 +52,11 @@ __device__ __forceinline__ uint32_t score_key(float f) {
   return f != f ? 0xffffffffu : k;
 }
 
+// The score of a key; not that of an unranked token (0), of a zero (which of the two) or of NaN.
+__device__ __forceinline__ float score_of(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
+
 struct SelShared {
   int cta_count[2];  // kept outright, equal to the threshold; read by the cluster
   int pick, rank;
@@ -181,7 +186,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     return make_uint4(k[0], k[1], k[2], k[3]);
   };
   if (held) {
-#pragma unroll 4
+#pragma unroll 8
     for (int t = w0 + 4 * lane; t < w1; t += 128) *reinterpret_cast<uint4*>(keys + (t - c0)) = load_keys(t);
   }
   __syncwarp();
@@ -250,37 +255,16 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   } else {
     prefix = 0xffffffffu;  // nothing is above it, and `rank` = 0 takes no tie
   }
-  // A token stays if held outright (sinks, recent, above the threshold) or among
-  // the first `rank` equal to it.  Four tokens of a lane: bit i of the low half:
-  // token t + i is kept outright, of the high half: it ties
-  auto kinds = [&](int t, const uint32_t(&kk)[4]) -> uint32_t {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (kk[i] > prefix) m |= 1u << i;
-      if (kk[i] == prefix) m |= 0x10000u << i;
-    }
-    if (t < lo || t + 3 >= m1) {  // not all ranked
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (t + i < w1 && (t + i < lo || t + i >= hi)) m |= 1u << i;
-    }
-    return m;
-  };
-  auto counts = [](uint32_t m) { return (uint32_t)__popc(m & 0xffffu) | (uint32_t)__popc(m >> 16) << 16; };
-  // every warp counts both kinds of its run ...
+  // A token stays if held outright (sinks, recent), above the threshold, or among
+  // the first `rank` equal to it: every warp counts both kinds of its run ...
   int takes = 0, ties = 0;
   for (int t = w0 + 4 * lane; t < w1; t += 128) {
     const uint4 k = keys_at(t);
-    const uint32_t m = kinds(t, {k.x, k.y, k.z, k.w});
-    takes += __popc(m & 0xffffu);
-    ties += __popc(m >> 16);
+    takes += (k.x > prefix) + (k.y > prefix) + (k.z > prefix) + (k.w > prefix);
+    ties += (k.x == prefix) + (k.y == prefix) + (k.z == prefix) + (k.w == prefix);
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    takes += __shfl_xor_sync(0xffffffffu, takes, o);
-    ties += __shfl_xor_sync(0xffffffffu, ties, o);
-  }
+  takes = __reduce_add_sync(0xffffffffu, takes) + max(0, min(w1, lo) - w0) + max(0, w1 - max(w0, hi));
+  ties = __reduce_add_sync(0xffffffffu, ties);
   if (lane == 0) {
     sh.warp_count[0][warp] = takes;
     sh.warp_count[1][warp] = ties;
@@ -299,35 +283,54 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   }
   takes += sum_before(sh.warp_count[0], warp, lane);
   ties += sum_before(sh.warp_count[1], warp, lane);
-  for (int t0 = w0; t0 < w1; t0 += 128) {
-    const int t = t0 + 4 * lane;
-    const uint4 k = t < w1 ? keys_at(t) : make_uint4(0, 0, 0, 0);
-    const uint32_t kk[4] = {k.x, k.y, k.z, k.w};
-    const uint32_t m = t < w1 ? kinds(t, kk) : 0u, c = counts(m);
-    if (!__any_sync(0xffffffffu, m != 0)) continue;
-    uint32_t inc = c;
+  const unsigned below = (1u << lane) - 1;
+  // 128 tokens at a time, four a lane; 32 at a time, where a ballot gives a token's
+  // place, for those with held tokens, ties, NaN, or a zero or negative threshold
+  for (int t1 = w0; t1 < w1; t1 += 128) {
+    const int t4 = t1 + 4 * lane;
+    const uint4 k4 = t4 < w1 ? keys_at(t4) : make_uint4(0, 0, 0, 0);
+    const uint32_t kk[4] = {k4.x, k4.y, k4.z, k4.w};
+    bool odd = prefix <= 0x80000000u;
+    int c = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
+    for (int i = 0; i < 4; ++i) {
+      odd |= kk[i] == prefix || kk[i] == 0xffffffffu;
+      c += kk[i] > prefix;
     }
-    int take_before = takes + (int)((inc - c) & 0xffffu), tie_before = ties + (int)((inc - c) >> 16);
-    if (m) {
+    if (t1 >= lo && min(t1 + 128, w1) <= hi && !__any_sync(0xffffffffu, odd)) {
+      int inc = c;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool take = m >> i & 1, tie = m >> (16 + i) & 1;
-        if (take || (tie && tie_before < rank)) {
-          const int j = take_before + min(tie_before, rank);
-          kept[j] = t + i;
-          out[j] = x[t + i];
-        }
-        take_before += take;
-        tie_before += tie;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
       }
+      int j = takes + min(ties, rank) + inc - c;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (kk[i] > prefix) {
+          kept[j] = t4 + i;
+          out[j] = score_of(kk[i]);
+          ++j;
+        }
+      takes += __shfl_sync(0xffffffffu, inc, 31);
+      continue;
     }
-    inc = __shfl_sync(0xffffffffu, inc, 31);
-    takes += (int)(inc & 0xffffu);
-    ties += (int)(inc >> 16);
+    for (int t0 = t1; t0 < min(t1 + 128, w1); t0 += 32) {
+      const int t = t0 + lane;
+      uint32_t key = 0;
+      if (t < w1) key = held ? keys[t - c0] : t >= m0 && t < m1 ? score_key(x[t]) : 0u;
+      const unsigned out_of = __ballot_sync(0xffffffffu, t < w1 && (t < lo || t >= hi));
+      const unsigned above = __ballot_sync(0xffffffffu, key > prefix) | out_of;
+      const unsigned tied = __ballot_sync(0xffffffffu, key == prefix);
+      const int tie_before = ties + __popc(tied & below);
+      if ((above >> lane & 1) || ((tied >> lane & 1) && tie_before < rank)) {
+        const int j = takes + __popc(above & below) + min(tie_before, rank);
+        kept[j] = t;
+        out[j] = x[t];
+      }
+      takes += __popc(above);
+      ties += __popc(tied);
+    }
   }
   if (C > 1) cluster_sync();  // no CTA leaves while another reads its counts
 }
