@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   SelHist& hi_ = *reinterpret_cast<SelHist*>(sel_smem + 4 * a.held_keys);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = (int)cluster_size(), rank_c = (int)cluster_rank();
+  griddep_wait();
   const int64_t row = blockIdx.x / C;
   const int s = (int)(row / a.b.Hkv), g = (int)(row % a.b.Hkv);
   const float* x = a.scores + row * a.max_tokens;
@@ -406,30 +407,11 @@ extern "C" pa_status pa_evict_tokens(const pa_sessions* b, const float* scores, 
   static std::atomic<uint64_t> allowed{0};
   if (!pa_allow_smem(pa::evict_select_kernel, 4 * (int)most_held + (int)sizeof(pa::SelHist), dev.index, allowed))
     return PA_ERR_CUDA;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(pairs * C));
-  cfg.blockDim = dim3(pa::kSelThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = cs;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = C;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, pa::evict_select_kernel, a) != cudaSuccess) return PA_ERR_CUDA;
+  if (!pa_launch_early(pa::evict_select_kernel, dim3((unsigned)(pairs * C)), dim3(pa::kSelThreads), smem, cs, C, a))
+    return PA_ERR_CUDA;
   const int rows = pa::kGatherThreads / (b->head_dim / 8);
   const int most = (int)(span < budget ? span : budget);
-  cudaLaunchConfig_t cg{};
-  cg.gridDim = dim3((most + rows - 1) / rows, b->num_kv_heads, b->n_sessions);
-  cg.blockDim = dim3(pa::kGatherThreads);
-  cg.stream = cs;
-  cudaLaunchAttribute ag{};
-  ag.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  ag.val.programmaticStreamSerializationAllowed = 1;
-  cg.attrs = &ag;
-  cg.numAttrs = 1;
-  const cudaError_t e = b->head_dim == 64 ? cudaLaunchKernelEx(&cg, pa::evict_gather_kernel<64>, a)
-                                          : cudaLaunchKernelEx(&cg, pa::evict_gather_kernel<128>, a);
-  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  const dim3 grid((most + rows - 1) / rows, b->num_kv_heads, b->n_sessions);
+  auto* gather = b->head_dim == 64 ? pa::evict_gather_kernel<64> : pa::evict_gather_kernel<128>;
+  return pa_launch_early(gather, grid, dim3(pa::kGatherThreads), 0, cs, 1, a) ? PA_OK : PA_ERR_CUDA;
 }

@@ -60,6 +60,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArg
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r0 = blockIdx.x * ROWS;
   const int pairs = a.R >> 1;
+  griddep_wait();
   for (int i = tid; i < ROWS * pairs; i += kRopeThreads) {
     const int j = i / pairs, p = i - j * pairs, r = r0 + j;
     if (r < a.b.rows) {
@@ -182,12 +183,7 @@ extern "C" pa_status pa_rope_append(const pa_sessions* b, const pa_rope* rope, c
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const bool many = b->num_rows >= 16 * pa_current_device().sms;
   const unsigned grid = many ? (b->num_rows + 3) / 4 : b->num_rows;
-  if (b->head_dim == 64) {
-    if (many) pa::rope_append_kernel<64, 4><<<grid, pa::kRopeThreads, 0, cs>>>(a);
-    else pa::rope_append_kernel<64, 1><<<grid, pa::kRopeThreads, 0, cs>>>(a);
-  } else {
-    if (many) pa::rope_append_kernel<128, 4><<<grid, pa::kRopeThreads, 0, cs>>>(a);
-    else pa::rope_append_kernel<128, 1><<<grid, pa::kRopeThreads, 0, cs>>>(a);
-  }
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  auto* kernel = b->head_dim == 64 ? (many ? pa::rope_append_kernel<64, 4> : pa::rope_append_kernel<64, 1>)
+                                   : (many ? pa::rope_append_kernel<128, 4> : pa::rope_append_kernel<128, 1>);
+  return pa_launch_early(kernel, dim3(grid), dim3(pa::kRopeThreads), 0, cs, 1, a) ? PA_OK : PA_ERR_CUDA;
 }

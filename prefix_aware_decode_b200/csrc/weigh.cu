@@ -20,10 +20,10 @@
 // scores in 512 tensor cycles; so a part of them is computed on the FMA pipe
 // (kFmaPairs), which leaves both pipes about equally busy.
 //
-// Roles (608 threads): warps 0-15 four groups of one thread per key, each with
+// Roles (640 threads): warps 0-15 four groups of one thread per key, each with
 // its own score buffer in tensor memory; warp 16 issues the products; warp 17
-// walks the items and loads the Q tiles and an item's first K block, warp 18 its
-// second (one warp took 3300 cycles to issue the copies of both).
+// walks the items and loads the Q tiles, warps 18 and 19 an item's first and
+// second K block (one warp took 3300 cycles an item to issue the copies of both).
 #include <type_traits>
 
 #include "ptx.cuh"
@@ -35,7 +35,7 @@ namespace pa {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kThreads = 608;
+constexpr int kThreads = 640;
 constexpr int kGroups = 1024;  // entries of the table of item prefixes
 constexpr int kQueue = 4;      // entries of the CTA's item queue
 constexpr int kFmaPairs = 4;   // of 16 pairs of scores: exponentials on the FMA pipe
@@ -145,6 +145,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [](uint64_t& b) { return smem_u32(&b); };
   const int step = 8 * a.pair;  // pages of an item
 
+  if (tid == 0) {
+    for (int i = 0; i < 8; ++i) {
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(bar(mi.kfull[b][i]), 1);
+        mbar_init(bar(mi.kempty[b][i]), 1);
+      }
+      mbar_init(bar(mi.qfull[i]), 2);               // the tile's bytes; the lse
+      mbar_init(bar(mi.qempty[i]), a.run ? 17 : 1 + 4 * a.pair);  // products; the warps that read the lse
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar(mi.sfull[i]), 1);
+      mbar_init(bar(mi.sempty[i]), 4);
+    }
+    for (int i = 0; i < kQueue; ++i) {
+      mbar_init(bar(mi.it_full[i]), 1);
+      mbar_init(bar(mi.it_empty[i]), 19);
+      mbar_init(bar(mi.comb[i]), 16);
+    }
+    mbar_init(bar(mi.done), 1);
+    mi.fail = 0;
+    fence_mbar_init();
+  }
+  if (warp == 16) tmem_alloc(smem_u32(&mi.tmem), 512);
+  griddep_wait();
+
   // ---------------- items before each group of sessions
   auto items_of = [&](int s) -> long long {
     if (s >= a.b.S) return 0;
@@ -172,30 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int w = 0; w < kThreads / 32; ++w) run += mi.warp_sum[w];
     __syncthreads();
   }
-  if (tid == 0) {
-    mi.prefix[groups] = run;
-    for (int i = 0; i < 8; ++i) {
-      for (int b = 0; b < 2; ++b) {
-        mbar_init(bar(mi.kfull[b][i]), 1);
-        mbar_init(bar(mi.kempty[b][i]), 1);
-      }
-      mbar_init(bar(mi.qfull[i]), 2);               // the tile's bytes; the lse
-      mbar_init(bar(mi.qempty[i]), a.run ? 17 : 1 + 4 * a.pair);  // products; the warps that read the lse
-    }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(bar(mi.sfull[i]), 1);
-      mbar_init(bar(mi.sempty[i]), 4);
-    }
-    for (int i = 0; i < kQueue; ++i) {
-      mbar_init(bar(mi.it_full[i]), 1);
-      mbar_init(bar(mi.it_empty[i]), 18);
-      mbar_init(bar(mi.comb[i]), 16);
-    }
-    mbar_init(bar(mi.done), 1);
-    mi.fail = 0;
-    fence_mbar_init();
-  }
-  if (warp == 16) tmem_alloc(smem_u32(&mi.tmem), 512);
+  if (tid == 0) mi.prefix[groups] = run;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -234,14 +236,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long span = a.run ? (total + gridDim.x - 1) / gridDim.x : 1;
     long long k = a.run ? blockIdx.x * span : blockIdx.x;
     const long long k_end = a.run ? min(total, k + span) : total, k_step = a.run ? 1 : gridDim.x;
-    const int oob = a.b.num_pages * a.b.Hkv * kPage;
-    int it = 0, n_k = 0, n_q = 0;
-    Ring kr, qr;
+    int it = 0, n_q = 0;
+    Ring qr;
     bool ok = true;
     int s = -1, g = 0, blk = 0, nblk = 0;
     Span x{};
     bool q_held = false;
-    int pg_next = -1;  // lane's page of the run's next item
     for (; k < k_end && ok; k += k_step) {
       // ---- item k: the next one of the run, or looked up
       bool same = false;
@@ -296,16 +296,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(bar(mi.it_full[e]));
       }
       ++it;
-      // ---- the first K block: lane l has its l-th page
-      auto page_of = [&](int v) -> int { return lane < 8 && v < x.np ? a.b.page(s, x.page_index(v)) : -1; };
-      const int pg = same ? pg_next : page_of(v0 + lane);
-      if (a.run && blk + 1 < nblk) pg_next = page_of(v0 + step + lane);
-      const int row = pg < 0 ? oob : (pg * a.b.Hkv + g) * kPage;
-      if (kr.phase > 0 && !(ok = wwait(mi.kempty[0][kr.slot], kr.phase - 1, 2))) break;
-      load_pages<S::HALVES>(smem_u32(tile_at(k_at(0, kr.slot))), &tk, row, 0, min(8, x.np - v0),
-                            bar(mi.kfull[0][kr.slot]), lead);
-      kr.next(a.nk);
-      ++n_k;
       // ---- Q tiles and their lse
       if (q_new) {
         for (int rt = one ? 0 : rt0; rt < (one ? 1 : rt1); ++rt) {
@@ -343,10 +333,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // loads in flight land before the CTA ends (all have, unless a wait gave up)
-    for (int i = max(0, n_k - a.nk); i < n_k; ++i) mbar_wait_bounded(bar(mi.kfull[0][i % a.nk]), (i / a.nk) & 1, kTimeoutNs);
     for (int i = max(0, n_q - a.nq); i < n_q; ++i) mbar_wait_bounded(bar(mi.qfull[i % a.nq]), (i / a.nq) & 1, kTimeoutNs);
-  } else if (warp == 18) {
-    // ---------------- the items' second K blocks
+  } else if (warp >= 18) {
+    // ---------------- the items' first (warp 18) and second K blocks
+    const int b = warp - 18;
     const bool lead = elect_one();
     const int oob = a.b.num_pages * a.b.Hkv * kPage;
     Ring kr;
@@ -360,17 +350,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(mi.it_empty[e]));
       if (v0 < 0) break;
-      if (a.pair < 2 || v0 + 8 >= x.np) continue;
-      const int v = v0 + 8 + lane;
+      if (b == 1 && (a.pair < 2 || v0 + 8 >= x.np)) continue;
+      const int v = v0 + 8 * b + lane;
       const int pg = lane < 8 && v < x.np ? a.b.page(s, x.page_index(v)) : -1;
       const int row = pg < 0 ? oob : (pg * a.b.Hkv + g) * kPage;
-      if (kr.phase > 0 && !wwait(mi.kempty[1][kr.slot], kr.phase - 1, 14)) break;
-      load_pages<S::HALVES>(smem_u32(tile_at(k_at(1, kr.slot))), &tk, row, 0, min(8, x.np - v0 - 8),
-                            bar(mi.kfull[1][kr.slot]), lead);
+      if (kr.phase > 0 && !wwait(mi.kempty[b][kr.slot], kr.phase - 1, 14)) break;
+      load_pages<S::HALVES>(smem_u32(tile_at(k_at(b, kr.slot))), &tk, row, 0, min(8, x.np - v0 - 8 * b),
+                            bar(mi.kfull[b][kr.slot]), lead);
       kr.next(a.nk);
       ++n_k;
     }
-    for (int i = max(0, n_k - a.nk); i < n_k; ++i) mbar_wait_bounded(bar(mi.kfull[1][i % a.nk]), (i / a.nk) & 1, kTimeoutNs);
+    for (int i = max(0, n_k - a.nk); i < n_k; ++i) mbar_wait_bounded(bar(mi.kfull[b][i % a.nk]), (i / a.nk) & 1, kTimeoutNs);
   } else if (warp == 16) {
     // ---------------- products (the whole warp walks, one elected lane issues)
     auto uni = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
@@ -605,8 +595,7 @@ pa_status launch(WeighArgs& a, const pa_sessions& b, const void* q, const void* 
   constexpr int smem = weigh_smem<D>();
   static std::atomic<uint64_t> allowed{0};
   if (!pa_allow_smem(weigh_kernel<D>, smem, dev.index, allowed)) return PA_ERR_CUDA;
-  weigh_kernel<D><<<grid, kThreads, smem, cs>>>(a, tq, tk);
-  return cudaGetLastError() == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  return pa_launch_early(weigh_kernel<D>, dim3(grid), dim3(kThreads), smem, cs, 1, a, tq, tk) ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace

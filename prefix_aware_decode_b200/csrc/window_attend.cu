@@ -183,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = Shape<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023) {  // the swizzle needs it; the kernel has no other shared memory before it
+    griddep_wait();
     if (threadIdx.x == 0) {
       a.desc[blockIdx.x].first = -1;
       record_status(a.status, PA_ERR_DEVICE, blockIdx.x, 0);
@@ -215,7 +216,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(mi.it_empty[i]), 9);  // product warp, 8 softmax warps
     }
     mi.fail = 0;
-    if (blockIdx.x == 0) *a.status = 0;
     fence_mbar_init();
   }
   if (warp == 9 && lane == 0) {
@@ -223,6 +223,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tk);
     prefetch_tmap(&tv);
   }
+
+  griddep_wait();
+  if (tid == 0 && blockIdx.x == 0) *a.status = 0;
 
   // ---------------- the line of blocks and this CTA's span
   const int heads = a.b.Hkv / a.lanes, in_lane = blockIdx.x % a.lanes;  // head k of the lane is k lanes + in_lane
@@ -923,19 +926,9 @@ bool launch(const pa::AttendArgs& a, const pa::Launch& l, const CUtensorMap& tq,
   constexpr int smem = pa::Shape<D>::SMEM;
   static std::atomic<uint64_t> allowed{0};
   if (!pa_allow_smem(k, smem, l.device, allowed)) return false;
-  k<<<l.grid, pa::kThreads, smem, cs>>>(a, tq, tk, tv);
-  if (cudaGetLastError() != cudaSuccess) return false;
+  if (!pa_launch_early(k, dim3(l.grid), dim3(pa::kThreads), smem, cs, 1, a, tq, tk, tv)) return false;
   if (l.grid == l.lanes || a.whole) return true;  // no item is cut
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(l.grid - l.lanes, pa::kJoinY);
-  cfg.blockDim = dim3(256);
-  cfg.stream = cs;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, pa::window_join_kernel<D>, a) == cudaSuccess;
+  return pa_launch_early(pa::window_join_kernel<D>, dim3(l.grid - l.lanes, pa::kJoinY), dim3(256), 0, cs, 1, a);
 }
 
 }  // namespace
