@@ -61,7 +61,14 @@ __device__ __forceinline__ int warp_find_session(const Sessions& b, int r, int l
 
 }  // namespace pa
 
-// Host side: checks of a pa_sessions that every operator makes.  `rows`: the
+// Host side: the rule of visibility.  Positions are below 2^30, so wider windows
+// and more sinks mean the same, and sums with them stay inside 32 bits.
+inline pa::Window pa_window(int32_t window, int32_t sinks) {
+  constexpr int32_t most = 1 << 30;
+  return pa::Window{window < most ? window : most, sinks < most ? sinks : most};
+}
+
+// Checks of a pa_sessions that every operator makes.  `rows`: the
 // operator uses the rows of the batch (cu_rows).
 inline pa_status pa_check_sessions(const pa_sessions* b, bool rows) {
   if (!b || b->n_sessions < 1 || b->max_pages < 1 || b->num_pages_in_pool < 1 || b->num_q_heads < 1 ||

@@ -612,7 +612,7 @@ extern "C" pa_status pa_weigh_tokens(const pa_sessions* b, int32_t window, int32
   if (!q || !k_pool || !lse || !pa_aligned16(q) || !pa_aligned16(k_pool)) return PA_ERR_INVALID;
   pa::WeighArgs a{};
   a.b = pa_device_sessions(*b);
-  a.w = pa::Window{window, sinks};
+  a.w = pa_window(window, sinks);
   const int G = b->num_q_heads / b->num_kv_heads;
   a.lg = G == 8 ? 3 : G == 4 ? 2 : G == 2 ? 1 : 0;
   a.lse = lse;

@@ -902,7 +902,7 @@ extern "C" pa_status pa_window_workspace_size(const pa_sessions* b, int32_t wind
   if (st != PA_OK) return st;
   if (!bytes || window < 0 || sinks < 0) return PA_ERR_INVALID;
   pa::Launch l;
-  if (!pa::plan_launch(*b, pa::Window{window, sinks}, &l)) return PA_ERR_UNSUPPORTED;
+  if (!pa::plan_launch(*b, pa_window(window, sinks), &l)) return PA_ERR_UNSUPPORTED;
   *bytes = l.bytes;
   return PA_OK;
 }
@@ -940,7 +940,7 @@ extern "C" pa_status pa_window_attend(const pa_sessions* b, int32_t window, int3
   if (st != PA_OK) return st;
   if (window < 0 || sinks < 0 || !(softmax_scale >= 0.f) || softmax_scale > 3.4e38f) return PA_ERR_INVALID;
   pa::Launch l;
-  if (!pa::plan_launch(*b, pa::Window{window, sinks}, &l)) return PA_ERR_UNSUPPORTED;
+  if (!pa::plan_launch(*b, pa_window(window, sinks), &l)) return PA_ERR_UNSUPPORTED;
   if (b->num_rows == 0) return PA_OK;
   if (!q || !k_pool || !v_pool || !out || !d_workspace) return PA_ERR_INVALID;
   if (!pa_aligned16(q) || !pa_aligned16(k_pool) || !pa_aligned16(v_pool) || !pa_aligned16(out) ||
@@ -949,7 +949,7 @@ extern "C" pa_status pa_window_attend(const pa_sessions* b, int32_t window, int3
   if (workspace_bytes < l.bytes) return PA_ERR_NOMEM;
   pa::AttendArgs a{};
   a.b = pa_device_sessions(*b);
-  a.w = pa::Window{window, sinks};
+  a.w = pa_window(window, sinks);
   a.lg = pa::log2_group(*b);
   a.slots = l.slots;
   a.min_span = l.min_span;

@@ -26,8 +26,8 @@ BATCHES = {
     "mixed": ([900, 20, 450], [1, 20, 200]),
     "no keys for some": ([3, 40, 0], [8, 2, 3]),  # more rows than cached tokens
 }
-HEADS = [(1, 1, 64), (8, 1, 128), (8, 2, 64), (4, 2, 128), (8, 8, 128), (32, 8, 128)]
-WINDOWS = [(0, 0), (1, 0), (16, 1), (37, 20), (100, 4), (1 << 30, 3), (5, 1000)]
+HEADS = [(1, 1, 64), (8, 1, 128), (8, 2, 64), (4, 2, 128), (8, 8, 128), (32, 8, 128), (12, 3, 64), (10, 5, 128)]
+WINDOWS = [(0, 0), (1, 0), (16, 1), (37, 20), (100, 4), (2 ** 31 - 1, 3), (5, 2 ** 31 - 1)]
 
 
 def _lib_status(name, *args):
@@ -183,6 +183,28 @@ def test_captured_calls_follow_the_device_arrays(n_rows):
             ref.check(lse[:big.n], l, ltol, "lse")
 
 
+@gpu
+def test_two_calls_at_once_and_their_status():
+    a, b = Cache([3000, 900], [200, 1], 8, 2, 128, seed=15), Cache([2000] * 3, [1, 1, 60], 8, 2, 128, seed=16)
+    want = [ref.run_attend(c) for c in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    calls = []
+    for c in (a, b):
+        args = c.dev("q", "k", "v", "table", "lens", "cu")
+        calls.append((args, pad.window_workspace(args[0], args[1], *args[3:])))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for (args, ws), s in zip(calls, streams):
+            got.append(pad.window_attend(*args, workspace=ws, stream=s))
+    torch.cuda.synchronize()
+    for i, (o, l) in enumerate(got):
+        assert torch.equal(o, want[i % 2][0]) and torch.equal(l, want[i % 2][1])
+    for (_, ws), s in zip(calls, streams):
+        assert pad.window_status(ws) == pad.window_status(ws, stream=s) == pad.PA_OK
+    assert pad.weigh_status() == pad.PA_OK
+
+
 # ------------------------------------------------------------------------------------------------ weights
 
 
@@ -235,6 +257,16 @@ def test_weigh_long_holes_and_a_short_score_row():
 def test_weigh_in_a_wide_table(batch, window, sinks, heads):
     # a table wide enough that the kernel takes key blocks in pairs
     _weigh_case(*BATCHES[batch], *heads, window, sinks, seed=28, extra_pages=700)
+
+
+@gpu
+def test_weigh_one_long_chunk_among_single_rows():
+    # few rows on average, so key blocks stream, but one session has several column tiles
+    rows = [1, 1, 150, 1, 0, 1, 1, 40, 1, 1]
+    kv = [300, 17, 420, 1, 50, 90, 512, 300, 33, 256]
+    for extra in (1, 700):
+        _weigh_case(kv, rows, 8, 2, 128, 0, 0, seed=30, extra_pages=extra)
+        _weigh_case(kv, rows, 8, 8, 64, 60, 9, seed=31, extra_pages=extra)
 
 
 @gpu
@@ -493,6 +525,52 @@ def test_a_session_lives_through_append_attend_weigh_and_evict():
     c.kv, c.table, c.num_pages, c.q, c.k, c.v = [int(t) for t in lens], torch.from_numpy(table), 64, q.cpu(), kp.cpu(), vp.cpu()
     tol = ref.attend(c)[2]
     ref.check(o2, o.double().cpu(), 2 * tol, "decode")
+
+
+@gpu
+def test_a_captured_step_of_all_four_follows_the_device_arrays():
+    """append, attend, weigh and evict in one graph, captured before any of them ran,
+    replayed as lengths, tables, positions and row offsets change in place."""
+    Hq, Hkv, D, budget = 8, 2, 128, 96
+    base = Cache([500, 300, 40], [3, 70, 1], Hq, Hkv, D, seed=50)
+    n = base.n
+    g = torch.Generator().manual_seed(51)
+    x = torch.randn(n, Hq + 2 * Hkv, D, generator=g).bfloat16().cuda()
+    inv = (10000.0 ** (-2.0 * torch.arange(D // 2, dtype=torch.float64) / D)).cuda()
+    spare = torch.zeros(3 * budget // P, Hkv, P, D).bfloat16()
+    dst = (base.num_pages + torch.arange(3 * budget // P).int()).view(3, -1).cuda()
+    pools = [torch.cat([t, spare]).cuda() for t in (base.k, base.v)]
+    table, lens, cu = base.dev("table", "lens", "cu")
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    scores = torch.zeros(3, Hkv, base.width * P, device="cuda")
+
+    def step(kp, vp, sc):
+        q = pad.rope_append(x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], pos, inv, kp, vp, table, lens, cu)
+        out, lse = pad.window_attend(q, kp, vp, table, lens, cu, window=200, sinks=4)
+        pad.weigh_tokens(q, kp, lse, table, lens, cu, sc, window=200, sinks=4)
+        return (q, out, lse, sc) + pad.evict_tokens(sc, kp, vp, table, lens, dst, budget, sinks=4, recent=20) + (kp, vp)
+
+    held = [t.clone() for t in pools] + [scores.clone()]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        res = step(*held)
+    for kv, rows in (([500, 300, 40], [3, 70, 1]), ([499, 17, 0], [1, 17, 0]), ([96, 300, 30], [20, 1, 30])):
+        lens.copy_(torch.tensor(kv, dtype=torch.int32))
+        cu.copy_(torch.tensor([0, rows[0], rows[0] + rows[1], sum(rows)], dtype=torch.int32))
+        pos.copy_(torch.randint(0, 5000, (n,), generator=g).int())
+        m = sum(rows)
+        for t, s in zip(held, pools + [scores]):
+            t.copy_(s)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = step(*[t.clone() for t in pools], scores.clone())
+        for i, (a, b) in enumerate(zip(res, want)):
+            if i < 3:
+                a, b = a[:m], b[:m]  # rows of no session are left as they were
+            assert torch.equal(a.view(torch.int16) if a.dtype == torch.bfloat16 else a,
+                               b.view(torch.int16) if b.dtype == torch.bfloat16 else b), i
+    del graph
 
 
 def test_session_pool_tables_and_compact():
