@@ -850,6 +850,170 @@ __global__ void __launch_bounds__(256) window_join_kernel(const AttendArgs a) {
   }
 }
 
+// ---------------- few rows over short caches
+//
+// One CTA per (row, kv head), each warp a page in turn, when a row sees at most
+// kShortPages pages: such a call is bound by its latency, and this form has a
+// fourth of the other's steps between launch and end (no tensor memory, no
+// roles, no join).  S (16 keys x 8 heads of the group) by warp-level products
+// (mma.sync; K rows straight from memory: the contraction may take the dims in
+// any order, so each lane's 16-byte piece serves two products); the weights in
+// fp32; P V on the CUDA cores, a warp per page, joined in shared memory.
+//
+// Taken up to 64 pages a row, groups of 4 and two rows a session on average.
+// Measured, this form against the other (device time of a call): 1 session of
+// 20 tokens, 8 heads of 64: 3.5 and 12.1 us; 4 of 300, 8/2 heads of 64: 7.2 and
+// 10.5 us; 16 of 500-1000, 32/8 heads of 128: 22.1 and 25.9 us; 64 of them 51.0
+// and 52.5 us (3.9 TB/s), 256 of 400-900 143 and 150 us; 256 of 100-900, 8/8
+// heads of 64, 63 and 118 us; 32 with a window of 500: 19.2 and 27.2 us.  Past the
+// rule the other wins: groups of 8, 8 sessions of 500-1000: 37.6 and 16.2 us (P V
+// on the CUDA cores); 3-4 rows a session, each a read of the same pages: 36.2 and
+// 30.3 us.
+constexpr int kShortPages = 64;
+constexpr int kShortThreads = 256, kShortWarps = kShortThreads / 32;
+
+template <int D, int G>
+__global__ void __launch_bounds__(kShortThreads) window_short_kernel(const AttendArgs a, const uint16_t* q,
+                                                                     const uint16_t* k_pool, const uint16_t* v_pool) {
+  constexpr int W = D / 32;              // dims of a lane in P V
+  __shared__ int pages[kShortPages];     // page id, -1: a hole
+  __shared__ float top[kShortWarps][8], sums[kShortWarps][8];
+  extern __shared__ __align__(16) float sm[];
+  float* weight = sm;                    // [16 np][G]
+  float* part = sm + a.slots * G;        // [kShortWarps][G][D]; slots: 16 x the most pages
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tq = lane & 3;
+  const int r = blockIdx.x, g = blockIdx.y;
+  griddep_wait();
+  if (r == 0 && g == 0 && tid == 0) *a.status = 0;
+  const int s = warp_find_session(a.b, r, lane);
+  const int r0 = a.b.row_begin(s), n = a.b.row_begin(s + 1) - r0;
+  if (r < r0 || r >= r0 + n) return;  // a row of no session
+  const int p = a.b.kv_len(s) - n + (r - r0);
+  // virtual pages 0 .. ns - 1 (sinks), then from page ns + off on, np in all
+  int np = 0, ns = 0, off = 0;
+  if (p >= 0) {
+    const int first = a.w.first(p) / kPage, sink = (min(a.w.sinks, p + 1) + kPage - 1) / kPage;
+    if (sink < first) ns = sink, off = first - sink;
+    np = p / kPage + 1 - off;
+  }
+  for (int v = tid; v < np; v += kShortThreads) pages[v] = a.b.page(s, v < ns ? v : v + off);
+  // the group's query rows as the second operand (heads past G: zeros)
+  const size_t row = ((size_t)r * a.b.Hq + g * G) * D;
+  uint4 qf[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i)
+    qf[i] = gr < G ? *reinterpret_cast<const uint4*>(q + row + gr * D + 32 * i + 8 * tq) : make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  float mx[2] = {-INFINITY, -INFINITY};  // of heads 2 tq, 2 tq + 1
+  for (int v = warp; v < np; v += kShortWarps) {
+    const int page = pages[v], t0 = (v < ns ? v : v + off) * kPage;
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+    if (page >= 0) {
+      const uint16_t* k = k_pool + (((size_t)page * a.b.Hkv + g) * kPage + gr) * D + 8 * tq;
+      uint4 k0[D / 32], k1[D / 32];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        k0[i] = *reinterpret_cast<const uint4*>(k + 32 * i);
+        k1[i] = *reinterpret_cast<const uint4*>(k + 8 * D + 32 * i);
+      }
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        mma_bf16_16816(x, {k0[i].x, k1[i].x, k0[i].y, k1[i].y}, qf[i].x, qf[i].y);
+        mma_bf16_16816(x, {k0[i].z, k1[i].z, k0[i].w, k1[i].w}, qf[i].z, qf[i].w);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // keys gr and gr + 8
+      const int key = gr + 8 * h;
+      const bool see = page >= 0 && a.w.sees(p, t0 + key);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float y = see ? x[2 * h + i] * a.scale_log2 : -INFINITY;
+        mx[i] = fmaxf(mx[i], y);
+        if (2 * tq + i < G) weight[(v * kPage + key) * G + 2 * tq + i] = y;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
+    if (gr == 0) top[warp][2 * tq + i] = mx[i];
+  }
+  __syncthreads();
+  float m[G], l[G], acc[G][W];
+#pragma unroll
+  for (int h = 0; h < G; ++h) {
+    m[h] = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kShortWarps; ++w) m[h] = fmaxf(m[h], top[w][h]);
+    l[h] = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) acc[h][i] = 0.f;
+  }
+  for (int v = warp; v < np; v += kShortWarps) {  // the warp's own scores
+    const int page = pages[v], t0 = (v < ns ? v : v + off) * kPage;
+    if (page < 0) continue;
+    for (int i = lane; i < kPage * G; i += 32) {
+      float mh = m[0];
+#pragma unroll
+      for (int h = 1; h < G; ++h) mh = i % G == h ? m[h] : mh;
+      float& w = weight[v * kPage * G + i];
+      w = w == -INFINITY ? 0.f : ex2(w - mh);
+    }
+    __syncwarp();
+    const uint16_t* vp = v_pool + ((size_t)page * a.b.Hkv + g) * kPage * D + lane * W;
+    // the page's V rows; those of tokens that the row does not see are not read
+    uint32_t raw[kPage][W / 2];
+#pragma unroll
+    for (int key = 0; key < kPage; ++key)
+#pragma unroll
+      for (int i = 0; i < W / 2; ++i)
+        raw[key][i] = a.w.sees(p, t0 + key) ? reinterpret_cast<const uint32_t*>(vp + key * D)[i] : 0u;
+#pragma unroll
+    for (int key = 0; key < kPage; ++key) {
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        const float w = weight[(v * kPage + key) * G + h];
+        l[h] += w;
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+          const float2 f = bf16x2_to_f2(raw[key][i]);
+          acc[h][2 * i] += w * f.x;
+          acc[h][2 * i + 1] += w * f.y;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < G; ++h) {
+    if (lane == 0) sums[warp][h] = l[h];
+#pragma unroll
+    for (int i = 0; i < W; ++i) part[(warp * G + h) * D + lane * W + i] = acc[h][i];
+  }
+  __syncthreads();
+  for (int i = 2 * tid; i < G * D; i += 2 * kShortThreads) {
+    const int h = i / D;
+    float sum = 0.f;
+    float2 o = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kShortWarps; ++w) {
+      sum += sums[w][h];
+      const float2 y = *reinterpret_cast<const float2*>(part + w * G * D + i);
+      o.x += y.x;
+      o.y += y.y;
+    }
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    *reinterpret_cast<uint32_t*>(a.out + row + i) = pack_bf16x2(o.x * inv, o.y * inv);
+    if (a.lse && i % D == 0) {
+      float mh = m[0];
+#pragma unroll
+      for (int k = 1; k < G; ++k) mh = h == k ? m[k] : mh;
+      a.lse[(size_t)r * a.b.Hq + g * G + h] = sum > 0.f ? (mh + lg2(sum)) * kLn2 : -INFINITY;
+    }
+  }
+}
+
 // log2 of G (1, 2, 4, 8)
 int log2_group(const pa_sessions& b) {
   const int G = b.num_q_heads / b.num_kv_heads;
@@ -858,6 +1022,7 @@ int log2_group(const pa_sessions& b) {
 
 struct Launch {
   int grid, slots, min_span, lanes, whole, device;
+  int short_pages;  // > 0: the form for few rows over short caches, of at most so many pages a row
   size_t off_desc, off_lse, off_o, bytes;
 };
 
@@ -869,8 +1034,10 @@ bool plan_launch(const pa_sessions& b, const Window& w, Launch* out) {
   const int T = 256 >> log2_group(b);
   const int64_t slots = (int64_t)b.num_rows / T + b.n_sessions;
   if (slots > (int64_t)kMaxChunks * kThreads) return false;
-  int64_t pages = b.max_pages;
+  int64_t pages = b.max_pages, row_pages = pages;
   if (w.window) {
+    const int64_t row_sees = ((int64_t)w.window + kPage - 2) / kPage + 1 + ((int64_t)w.sinks + kPage - 1) / kPage;
+    if (row_sees < row_pages) row_pages = row_sees;
     const int64_t seen = ((int64_t)w.window + T + kPage - 2) / kPage + 1 + ((int64_t)w.sinks + kPage - 1) / kPage + 1;
     if (seen < pages) pages = seen;
   }
@@ -886,6 +1053,8 @@ bool plan_launch(const pa_sessions& b, const Window& w, Launch* out) {
   if (spans > most) spans = most;
   if (spans < 1) spans = 1;
   out->grid = (int)spans * out->lanes;
+  out->short_pages = 0;
+  if (row_pages <= kShortPages && log2_group(b) <= 2 && b.num_rows <= 2 * b.n_sessions) out->short_pages = (int)row_pages;
   out->slots = (int)slots;
   out->off_desc = 256;
   out->off_lse = out->off_desc + ((size_t)out->grid * sizeof(Desc) + 255) / 256 * 256;
@@ -918,6 +1087,25 @@ extern "C" pa_status pa_window_status(const void* d_workspace, void* stream, pa_
 }
 
 namespace {
+
+template <int D, int G>
+bool launch_short(pa::AttendArgs a, int pages, const void* q, const void* k_pool, const void* v_pool, cudaStream_t cs) {
+  a.slots = 16 * pages;
+  const int smem = 4 * G * (a.slots + pa::kShortWarps * D);  // at most 32 KB
+  return pa_launch_early(pa::window_short_kernel<D, G>, dim3(a.b.rows, a.b.Hkv), dim3(pa::kShortThreads), smem, cs, 1, a,
+                         static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k_pool),
+                         static_cast<const uint16_t*>(v_pool));
+}
+
+template <int D>
+bool launch_short(const pa::AttendArgs& a, int pages, const void* q, const void* k_pool, const void* v_pool,
+                  cudaStream_t cs) {
+  switch (a.lg) {
+    case 0: return launch_short<D, 1>(a, pages, q, k_pool, v_pool, cs);
+    case 1: return launch_short<D, 2>(a, pages, q, k_pool, v_pool, cs);
+    default: return launch_short<D, 4>(a, pages, q, k_pool, v_pool, cs);
+  }
+}
 
 template <int D>
 bool launch(const pa::AttendArgs& a, const pa::Launch& l, const CUtensorMap& tq, const CUtensorMap& tk,
@@ -964,11 +1152,16 @@ extern "C" pa_status pa_window_attend(const pa_sessions* b, int32_t window, int3
   a.part_lse = reinterpret_cast<float*>(ws + l.off_lse);
   a.part_o = reinterpret_cast<float*>(ws + l.off_o);
   const int D = b->head_dim, G = 1 << a.lg;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (l.short_pages > 0) {
+    const bool ok = D == 64 ? launch_short<64>(a, l.short_pages, q, k_pool, v_pool, cs)
+                            : launch_short<128>(a, l.short_pages, q, k_pool, v_pool, cs);
+    return ok ? PA_OK : PA_ERR_CUDA;
+  }
   CUtensorMap tq, tk, tv;
   if (!pa::tmap_q(&tq, q, b->num_rows, b->num_q_heads, D, G, 128 / G) ||
       !pa::tmap_pool(&tk, k_pool, b->num_pages_in_pool, b->num_kv_heads, D) ||
       !pa::tmap_pool(&tv, v_pool, b->num_pages_in_pool, b->num_kv_heads, D))
     return PA_ERR_CUDA;
-  cudaStream_t cs = static_cast<cudaStream_t>(stream);
   return (D == 64 ? launch<64>(a, l, tq, tk, tv, cs) : launch<128>(a, l, tq, tk, tv, cs)) ? PA_OK : PA_ERR_CUDA;
 }

@@ -37,8 +37,8 @@ def _lib_status(name, *args):
 # ------------------------------------------------------------------------------------------------ attention
 
 
-def _attend_case(kv, rows, Hq, Hkv, D, window, sinks, seed=0, holes=(), scale=0.0):
-    c = Cache(kv, rows, Hq, Hkv, D, seed=seed, holes=holes, extra_rows=2)
+def _attend_case(kv, rows, Hq, Hkv, D, window, sinks, seed=0, holes=(), scale=0.0, extra_pages=1):
+    c = Cache(kv, rows, Hq, Hkv, D, seed=seed, holes=holes, extra_rows=2, extra_pages=extra_pages)
     out = torch.full((c.n + 2, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
     lse = torch.full((c.n + 2, Hq), 7.0, device="cuda")
     ref.run_attend(c, window, sinks, scale, out=out, lse=lse)
@@ -62,6 +62,46 @@ def test_attend_batches_and_windows(batch, window, sinks):
 def test_attend_head_layouts(batch, heads):
     _attend_case(*BATCHES[batch], *heads, 0, 0, seed=2)
     _attend_case(*BATCHES[batch], *heads, 130, 5, seed=3)
+
+
+# a table of more than 64 pages a session, or more than two rows of each, takes the
+# form for long caches; the same rows with a narrow table the one for short ones
+@gpu
+@pytest.mark.parametrize("extra_pages", [1, 80])
+@pytest.mark.parametrize("heads", [(8, 8, 64), (4, 2, 128), (8, 2, 128), (16, 4, 64), (8, 1, 64)])
+@pytest.mark.parametrize("kv,rows,holes", [
+    ([17, 33, 5, 300, 16], [1, 1, 1, 1, 1], ()),
+    ([1, 0, 64, 1, 990], [1, 2, 0, 3, 2], ()),  # rows without keys, a session without rows
+    ([200, 150, 31], [1, 2, 1], [(0, 0), (0, 5), (1, 3), (1, 9), (0, 12), (2, 0), (2, 1)]),
+])
+def test_attend_short_and_long_tables(kv, rows, holes, heads, extra_pages):
+    _attend_case(kv, rows, *heads, 0, 0, seed=6, holes=holes, extra_pages=extra_pages)
+    _attend_case(kv, rows, *heads, 0, 0, seed=7, holes=holes, extra_pages=extra_pages, scale=0.7)
+
+
+@gpu
+@pytest.mark.parametrize("window,sinks", [(1, 0), (15, 1), (16, 16), (17, 33), (500, 20), (975, 17), (976, 33)])
+def test_attend_short_windows_over_long_caches(window, sinks):
+    # up to 64 pages a row: the windows' edges inside pages, sinks that meet the window
+    kv, rows = [2000, 40, 1003, 17, 530], [2, 1, 2, 1, 2]
+    _attend_case(kv, rows, 8, 2, 64, window, sinks, seed=8)
+    _attend_case(kv, rows, 3, 3, 128, window, sinks, seed=9, holes=[(0, 0), (0, 124), (2, 40)])
+
+
+@gpu
+def test_attend_short_form_keeps_out_what_no_row_sees_and_resets_the_status():
+    c = Cache([400, 20], [1, 1], 8, 2, 128, seed=12)
+    want = ref.attend(c, 100, 4)
+    for t in range(4, 300):
+        c.k[c.table[0, t // P].item(), :, t % P] = math.nan
+        c.v[c.table[0, t // P].item(), :, t % P] = math.inf
+    q, k, table, lens, cu = c.dev("q", "k", "table", "lens", "cu")
+    ws = pad.window_workspace(q, k, table, lens, cu, window=100, sinks=4)
+    ws.view(torch.uint8).fill_(255)
+    out, lse = ref.run_attend(c, 100, 4, workspace=ws)
+    assert pad.window_status(ws) == pad.PA_OK
+    ref.check(out, want[0], want[2], "out")
+    ref.check(lse, want[1], want[3], "lse")
 
 
 @gpu
