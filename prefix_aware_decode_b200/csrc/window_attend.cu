@@ -855,32 +855,34 @@ __global__ void __launch_bounds__(256) window_join_kernel(const AttendArgs a) {
 // One CTA per (row, kv head), each warp a page in turn, when a row sees at most
 // kShortPages pages: such a call is bound by its latency, and this form has a
 // fourth of the other's steps between launch and end (no tensor memory, no
-// roles, no join).  S (16 keys x 8 heads of the group) by warp-level products
-// (mma.sync; K rows straight from memory: the contraction may take the dims in
-// any order, so each lane's 16-byte piece serves two products); the weights in
-// fp32; P V on the CUDA cores, a warp per page, joined in shared memory.
+// roles, no join).  A warp keeps its own running maxima and sums (fp32), so K and
+// V of its next page are in flight while it works on one.  S (16 keys x 8 heads
+// of the group) by warp-level products (mma.sync; K rows straight from memory:
+// the contraction may take the dims in any order, so each lane's 16-byte piece
+// serves two products); the weights stay in fp32; P V on the CUDA cores; the
+// warps' results are joined in shared memory.
 //
 // Taken up to 64 pages a row, groups of 4 and two rows a session on average.
 // Measured, this form against the other (device time of a call): 1 session of
-// 20 tokens, 8 heads of 64: 3.5 and 12.1 us; 4 of 300, 8/2 heads of 64: 7.2 and
-// 10.5 us; 16 of 500-1000, 32/8 heads of 128: 22.1 and 25.9 us; 64 of them 51.0
-// and 52.5 us (3.9 TB/s), 256 of 400-900 143 and 150 us; 256 of 100-900, 8/8
-// heads of 64, 63 and 118 us; 32 with a window of 500: 19.2 and 27.2 us.  Past the
-// rule the other wins: groups of 8, 8 sessions of 500-1000: 37.6 and 16.2 us (P V
-// on the CUDA cores); 3-4 rows a session, each a read of the same pages: 36.2 and
-// 30.3 us.
+// 20 tokens, 8 heads of 64: 2.5 and 11.8 us; 4 of 300, 8/2 heads of 64: 4.9 and
+// 10.3 us; 16 of 500-1000, 32/8 heads of 128: 19.3 and 26.1 us; 64 of them 45.7
+// and 53.1 us (4.4 TB/s), 256 of 400-900 127 and 149 us (5.4 TB/s); 256 of
+// 100-900, 8/8 heads of 64, 56 and 117 us.  Past the rule the other wins: 4
+// sessions of 1500-2000, 32/8 heads: 29.4 and 19.6 us; groups of 8, 8 sessions
+// of 500-1000: 20.8 and 16.2 us; 3-4 rows a session, each a read of the same
+// pages, 33.5 and 30.1 us.
 constexpr int kShortPages = 64;
 constexpr int kShortThreads = 256, kShortWarps = kShortThreads / 32;
 
 template <int D, int G>
-__global__ void __launch_bounds__(kShortThreads) window_short_kernel(const AttendArgs a, const uint16_t* q,
-                                                                     const uint16_t* k_pool, const uint16_t* v_pool) {
-  constexpr int W = D / 32;              // dims of a lane in P V
-  __shared__ int pages[kShortPages];     // page id, -1: a hole
+__global__ void __launch_bounds__(kShortThreads, 2) window_short_kernel(const AttendArgs a, const uint16_t* __restrict__ q,
+                                                                        const uint16_t* __restrict__ k_pool,
+                                                                        const uint16_t* __restrict__ v_pool) {
+  constexpr int W = D / 32;  // dims of a lane in P V
+  __shared__ __align__(16) float weight[kShortWarps][kPage][G];  // of the warp's page
+  __shared__ float scale[kShortWarps][8];                        // of what the warp holds, for a new maximum
   __shared__ float top[kShortWarps][8], sums[kShortWarps][8];
-  extern __shared__ __align__(16) float sm[];
-  float* weight = sm;                    // [16 np][G]
-  float* part = sm + a.slots * G;        // [kShortWarps][G][D]; slots: 16 x the most pages
+  __shared__ __align__(16) float part[kShortWarps][G][D];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tq = lane & 3;
   const int r = blockIdx.x, g = blockIdx.y;
   griddep_wait();
@@ -896,86 +898,92 @@ __global__ void __launch_bounds__(kShortThreads) window_short_kernel(const Atten
     if (sink < first) ns = sink, off = first - sink;
     np = p / kPage + 1 - off;
   }
-  for (int v = tid; v < np; v += kShortThreads) pages[v] = a.b.page(s, v < ns ? v : v + off);
+  auto logical = [&](int v) { return v < ns ? v : v + off; };
+  // lane j: the page id of the warp's j-th page (-1: a hole)
+  const int mine = warp + kShortWarps * lane < np ? a.b.page(s, logical(warp + kShortWarps * lane)) : -1;
   // the group's query rows as the second operand (heads past G: zeros)
   const size_t row = ((size_t)r * a.b.Hq + g * G) * D;
   uint4 qf[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
-    qf[i] = gr < G ? *reinterpret_cast<const uint4*>(q + row + gr * D + 32 * i + 8 * tq) : make_uint4(0, 0, 0, 0);
-  __syncthreads();
-  float mx[2] = {-INFINITY, -INFINITY};  // of heads 2 tq, 2 tq + 1
-  for (int v = warp; v < np; v += kShortWarps) {
-    const int page = pages[v], t0 = (v < ns ? v : v + off) * kPage;
+    qf[i] = gr < G ? __ldg(reinterpret_cast<const uint4*>(q + row + gr * D + 32 * i + 8 * tq)) : make_uint4(0, 0, 0, 0);
+  uint4 k0[D / 32], k1[D / 32];  // rows gr and gr + 8 of the page's keys
+  uint32_t raw[kPage][W / 2];    // its V rows; those that the row does not see are not read
+  auto load_k = [&](int page) {
+    if (page < 0) return;
+    const uint16_t* k = k_pool + (((size_t)page * a.b.Hkv + g) * kPage + gr) * D + 8 * tq;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      k0[i] = __ldg(reinterpret_cast<const uint4*>(k + 32 * i));
+      k1[i] = __ldg(reinterpret_cast<const uint4*>(k + 8 * D + 32 * i));
+    }
+  };
+  auto load_v = [&](int page, int t0) {
+    if (page < 0) return;
+    const uint16_t* vp = v_pool + ((size_t)page * a.b.Hkv + g) * kPage * D + lane * W;
+#pragma unroll
+    for (int key = 0; key < kPage; ++key) {
+      const bool see = a.w.sees(p, t0 + key);
+      if (W == 2) {
+        raw[key][0] = see ? __ldg(reinterpret_cast<const uint32_t*>(vp + key * D)) : 0u;
+      } else {
+        const uint2 y = see ? __ldg(reinterpret_cast<const uint2*>(vp + key * D)) : make_uint2(0u, 0u);
+        raw[key][0] = y.x;
+        raw[key][W / 2 - 1] = y.y;
+      }
+    }
+  };
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // of heads 2 tq, 2 tq + 1; l: of this lane's keys
+  float acc[G][W] = {};
+  int page = __shfl_sync(0xffffffffu, mine, 0);
+  load_k(page);
+  load_v(page, logical(warp) * kPage);
+  for (int v = warp, j = 0; v < np; v += kShortWarps) {
+    const int t0 = logical(v) * kPage, next = __shfl_sync(0xffffffffu, mine, ++j & 31);
+    const int t1 = logical(v + kShortWarps) * kPage;
+    if (page < 0) {  // nothing to see: on to the next
+      page = next;
+      load_k(page);
+      load_v(page, t1);
+      continue;
+    }
     float x[4] = {0.f, 0.f, 0.f, 0.f};
-    if (page >= 0) {
-      const uint16_t* k = k_pool + (((size_t)page * a.b.Hkv + g) * kPage + gr) * D + 8 * tq;
-      uint4 k0[D / 32], k1[D / 32];
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        k0[i] = *reinterpret_cast<const uint4*>(k + 32 * i);
-        k1[i] = *reinterpret_cast<const uint4*>(k + 8 * D + 32 * i);
-      }
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        mma_bf16_16816(x, {k0[i].x, k1[i].x, k0[i].y, k1[i].y}, qf[i].x, qf[i].y);
-        mma_bf16_16816(x, {k0[i].z, k1[i].z, k0[i].w, k1[i].w}, qf[i].z, qf[i].w);
-      }
+    for (int i = 0; i < D / 32; ++i) {
+      mma_bf16_16816(x, {k0[i].x, k1[i].x, k0[i].y, k1[i].y}, qf[i].x, qf[i].y);
+      mma_bf16_16816(x, {k0[i].z, k1[i].z, k0[i].w, k1[i].w}, qf[i].z, qf[i].w);
     }
+    load_k(next);
+    const bool see0 = a.w.sees(p, t0 + gr), see1 = a.w.sees(p, t0 + gr + 8);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {  // keys gr and gr + 8
-      const int key = gr + 8 * h;
-      const bool see = page >= 0 && a.w.sees(p, t0 + key);
+    for (int i = 0; i < 2; ++i) {
+      const float y0 = see0 ? x[i] * a.scale_log2 : -INFINITY, y1 = see1 ? x[2 + i] * a.scale_log2 : -INFINITY;
+      float mx = fmaxf(y0, y1);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float y = see ? x[2 * h + i] * a.scale_log2 : -INFINITY;
-        mx[i] = fmaxf(mx[i], y);
-        if (2 * tq + i < G) weight[(v * kPage + key) * G + 2 * tq + i] = y;
+      for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      mx = fmaxf(mx, m[i]);
+      const float c = m[i] == mx ? 1.f : ex2(m[i] - mx);  // no key yet: 0, of nothing
+      const float w0 = y0 == -INFINITY ? 0.f : ex2(y0 - mx), w1 = y1 == -INFINITY ? 0.f : ex2(y1 - mx);
+      m[i] = mx;
+      l[i] = l[i] * c + w0 + w1;
+      if (2 * tq + i < G) {
+        weight[warp][gr][2 * tq + i] = w0;
+        weight[warp][gr + 8][2 * tq + i] = w1;
+        if (gr == 0) scale[warp][2 * tq + i] = c;
       }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
-    if (gr == 0) top[warp][2 * tq + i] = mx[i];
-  }
-  __syncthreads();
-  float m[G], l[G], acc[G][W];
-#pragma unroll
-  for (int h = 0; h < G; ++h) {
-    m[h] = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kShortWarps; ++w) m[h] = fmaxf(m[h], top[w][h]);
-    l[h] = 0.f;
-#pragma unroll
-    for (int i = 0; i < W; ++i) acc[h][i] = 0.f;
-  }
-  for (int v = warp; v < np; v += kShortWarps) {  // the warp's own scores
-    const int page = pages[v], t0 = (v < ns ? v : v + off) * kPage;
-    if (page < 0) continue;
-    for (int i = lane; i < kPage * G; i += 32) {
-      float mh = m[0];
-#pragma unroll
-      for (int h = 1; h < G; ++h) mh = i % G == h ? m[h] : mh;
-      float& w = weight[v * kPage * G + i];
-      w = w == -INFINITY ? 0.f : ex2(w - mh);
     }
     __syncwarp();
-    const uint16_t* vp = v_pool + ((size_t)page * a.b.Hkv + g) * kPage * D + lane * W;
-    // the page's V rows; those of tokens that the row does not see are not read
-    uint32_t raw[kPage][W / 2];
 #pragma unroll
-    for (int key = 0; key < kPage; ++key)
+    for (int h = 0; h < G; ++h) {
+      const float c = scale[warp][h];
 #pragma unroll
-      for (int i = 0; i < W / 2; ++i)
-        raw[key][i] = a.w.sees(p, t0 + key) ? reinterpret_cast<const uint32_t*>(vp + key * D)[i] : 0u;
+      for (int i = 0; i < W; ++i) acc[h][i] *= c;
+    }
 #pragma unroll
     for (int key = 0; key < kPage; ++key) {
 #pragma unroll
       for (int h = 0; h < G; ++h) {
-        const float w = weight[(v * kPage + key) * G + h];
-        l[h] += w;
+        const float w = weight[warp][key][h];
 #pragma unroll
         for (int i = 0; i < W / 2; ++i) {
           const float2 f = bf16x2_to_f2(raw[key][i]);
@@ -984,33 +992,38 @@ __global__ void __launch_bounds__(kShortThreads) window_short_kernel(const Atten
         }
       }
     }
+    page = next;
+    load_v(page, t1);
+    __syncwarp();  // the weights are read
   }
 #pragma unroll
-  for (int h = 0; h < G; ++h) {
-    if (lane == 0) sums[warp][h] = l[h];
+  for (int i = 0; i < 2; ++i) {
 #pragma unroll
-    for (int i = 0; i < W; ++i) part[(warp * G + h) * D + lane * W + i] = acc[h][i];
+    for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+    if (gr == 0) top[warp][2 * tq + i] = m[i], sums[warp][2 * tq + i] = l[i];
   }
+#pragma unroll
+  for (int h = 0; h < G; ++h)
+#pragma unroll
+    for (int i = 0; i < W; ++i) part[warp][h][lane * W + i] = acc[h][i];
   __syncthreads();
   for (int i = 2 * tid; i < G * D; i += 2 * kShortThreads) {
     const int h = i / D;
-    float sum = 0.f;
+    float mx = -INFINITY, sum = 0.f;
     float2 o = make_float2(0.f, 0.f);
 #pragma unroll
+    for (int w = 0; w < kShortWarps; ++w) mx = fmaxf(mx, top[w][h]);
+#pragma unroll
     for (int w = 0; w < kShortWarps; ++w) {
-      sum += sums[w][h];
-      const float2 y = *reinterpret_cast<const float2*>(part + w * G * D + i);
-      o.x += y.x;
-      o.y += y.y;
+      const float f = top[w][h] == -INFINITY ? 0.f : ex2(top[w][h] - mx);
+      const float2 y = *reinterpret_cast<const float2*>(&part[w][h][i % D]);
+      sum += f * sums[w][h];
+      o.x += f * y.x;
+      o.y += f * y.y;
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     *reinterpret_cast<uint32_t*>(a.out + row + i) = pack_bf16x2(o.x * inv, o.y * inv);
-    if (a.lse && i % D == 0) {
-      float mh = m[0];
-#pragma unroll
-      for (int k = 1; k < G; ++k) mh = h == k ? m[k] : mh;
-      a.lse[(size_t)r * a.b.Hq + g * G + h] = sum > 0.f ? (mh + lg2(sum)) * kLn2 : -INFINITY;
-    }
+    if (a.lse && i % D == 0) a.lse[(size_t)r * a.b.Hq + g * G + h] = sum > 0.f ? (mx + lg2(sum)) * kLn2 : -INFINITY;
   }
 }
 
@@ -1022,7 +1035,7 @@ int log2_group(const pa_sessions& b) {
 
 struct Launch {
   int grid, slots, min_span, lanes, whole, device;
-  int short_pages;  // > 0: the form for few rows over short caches, of at most so many pages a row
+  bool short_rows;  // the form for few rows over short caches
   size_t off_desc, off_lse, off_o, bytes;
 };
 
@@ -1053,8 +1066,7 @@ bool plan_launch(const pa_sessions& b, const Window& w, Launch* out) {
   if (spans > most) spans = most;
   if (spans < 1) spans = 1;
   out->grid = (int)spans * out->lanes;
-  out->short_pages = 0;
-  if (row_pages <= kShortPages && log2_group(b) <= 2 && b.num_rows <= 2 * b.n_sessions) out->short_pages = (int)row_pages;
+  out->short_rows = row_pages <= kShortPages && log2_group(b) <= 2 && b.num_rows <= 2 * b.n_sessions;
   out->slots = (int)slots;
   out->off_desc = 256;
   out->off_lse = out->off_desc + ((size_t)out->grid * sizeof(Desc) + 255) / 256 * 256;
@@ -1089,21 +1101,18 @@ extern "C" pa_status pa_window_status(const void* d_workspace, void* stream, pa_
 namespace {
 
 template <int D, int G>
-bool launch_short(pa::AttendArgs a, int pages, const void* q, const void* k_pool, const void* v_pool, cudaStream_t cs) {
-  a.slots = 16 * pages;
-  const int smem = 4 * G * (a.slots + pa::kShortWarps * D);  // at most 32 KB
-  return pa_launch_early(pa::window_short_kernel<D, G>, dim3(a.b.rows, a.b.Hkv), dim3(pa::kShortThreads), smem, cs, 1, a,
+bool launch_short(const pa::AttendArgs& a, const void* q, const void* k_pool, const void* v_pool, cudaStream_t cs) {
+  return pa_launch_early(pa::window_short_kernel<D, G>, dim3(a.b.rows, a.b.Hkv), dim3(pa::kShortThreads), 0, cs, 1, a,
                          static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k_pool),
                          static_cast<const uint16_t*>(v_pool));
 }
 
 template <int D>
-bool launch_short(const pa::AttendArgs& a, int pages, const void* q, const void* k_pool, const void* v_pool,
-                  cudaStream_t cs) {
+bool launch_short(const pa::AttendArgs& a, const void* q, const void* k_pool, const void* v_pool, cudaStream_t cs) {
   switch (a.lg) {
-    case 0: return launch_short<D, 1>(a, pages, q, k_pool, v_pool, cs);
-    case 1: return launch_short<D, 2>(a, pages, q, k_pool, v_pool, cs);
-    default: return launch_short<D, 4>(a, pages, q, k_pool, v_pool, cs);
+    case 0: return launch_short<D, 1>(a, q, k_pool, v_pool, cs);
+    case 1: return launch_short<D, 2>(a, q, k_pool, v_pool, cs);
+    default: return launch_short<D, 4>(a, q, k_pool, v_pool, cs);
   }
 }
 
@@ -1153,9 +1162,8 @@ extern "C" pa_status pa_window_attend(const pa_sessions* b, int32_t window, int3
   a.part_o = reinterpret_cast<float*>(ws + l.off_o);
   const int D = b->head_dim, G = 1 << a.lg;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (l.short_pages > 0) {
-    const bool ok = D == 64 ? launch_short<64>(a, l.short_pages, q, k_pool, v_pool, cs)
-                            : launch_short<128>(a, l.short_pages, q, k_pool, v_pool, cs);
+  if (l.short_rows) {
+    const bool ok = D == 64 ? launch_short<64>(a, q, k_pool, v_pool, cs) : launch_short<128>(a, q, k_pool, v_pool, cs);
     return ok ? PA_OK : PA_ERR_CUDA;
   }
   CUtensorMap tq, tk, tv;
