@@ -68,28 +68,6 @@ struct SelHist {
   int cta_hist[2][kBins];  // by parity of the pass; read by the cluster
 };
 
-__device__ __forceinline__ unsigned cluster_rank() {
-  unsigned r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ unsigned cluster_size() {
-  unsigned r;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
-}
-// An int of this CTA's shared memory as CTA `rank` of the cluster has it.
-__device__ __forceinline__ int cluster_read(const int* p, unsigned rank) {
-  uint32_t at;
-  int v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-  return v;
-}
-
 // Sum of the first n <= 32 of v, by a whole warp.
 __device__ __forceinline__ int sum_before(const int* v, int n, int lane) {
   return __reduce_add_sync(0xffffffffu, lane < n ? v[lane] : 0);

@@ -9,6 +9,7 @@
 #include <cstdint>
 
 #include "pa.h"
+#include "ptx.cuh"
 
 namespace pa {
 
@@ -57,6 +58,30 @@ __device__ __forceinline__ int warp_find_session(const Sessions& b, int r, int l
     lo += k * step;
   }
   return lo;
+}
+
+// A cluster of CTAs and its shared memory.
+__device__ __forceinline__ unsigned cluster_rank() {
+  unsigned r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ unsigned cluster_size() {
+  unsigned r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// A word of this CTA's shared memory as CTA `rank` of the cluster has it.
+template <typename T>
+__device__ __forceinline__ T cluster_read(const T* p, unsigned rank) {
+  static_assert(sizeof(T) == 4);
+  uint32_t at, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return *reinterpret_cast<T*>(&v);
 }
 
 }  // namespace pa

@@ -852,26 +852,30 @@ __global__ void __launch_bounds__(256) window_join_kernel(const AttendArgs a) {
 
 // ---------------- few rows over short caches
 //
-// One CTA per (row, kv head), each warp a page in turn, when a row sees at most
-// kShortPages pages: such a call is bound by its latency, and this form has a
-// fourth of the other's steps between launch and end (no tensor memory, no
-// roles, no join).  A warp keeps its own running maxima and sums (fp32), so K and
-// V of its next page are in flight while it works on one.  S (16 keys x 8 heads
-// of the group) by warp-level products (mma.sync; K rows straight from memory:
-// the contraction may take the dims in any order, so each lane's 16-byte piece
-// serves two products); the weights stay in fp32; P V on the CUDA cores; the
-// warps' results are joined in shared memory.
+// One CTA per (row, kv head), or a cluster of up to 8 when that leaves SMs free,
+// each warp a page in turn: such a call is bound by its latency, and this form
+// has a fourth of the other's steps between launch and end (no tensor memory, no
+// roles, no join launch).  A warp keeps its own running maxima and sums (fp32), so
+// K and V of its next page are in flight while it works on one.  S (16 keys x 8
+// heads of the group) by warp-level products (mma.sync; K rows straight from
+// memory: the contraction may take the dims in any order, so each lane's 16-byte
+// piece serves two products); the weights stay in fp32; P V on the CUDA cores; the
+// warps' results are joined in shared memory, the CTAs' through the cluster's.
 //
-// Taken up to 64 pages a row, groups of 4 and two rows a session on average.
-// Measured, this form against the other (device time of a call): 1 session of
-// 20 tokens, 8 heads of 64: 2.5 and 11.8 us; 4 of 300, 8/2 heads of 64: 4.9 and
-// 10.3 us; 16 of 500-1000, 32/8 heads of 128: 19.3 and 26.1 us; 64 of them 45.7
-// and 53.1 us (4.4 TB/s), 256 of 400-900 127 and 149 us (5.4 TB/s); 256 of
-// 100-900, 8/8 heads of 64, 56 and 117 us.  Past the rule the other wins: 4
-// sessions of 1500-2000, 32/8 heads: 29.4 and 19.6 us; groups of 8, 8 sessions
-// of 500-1000: 20.8 and 16.2 us; 3-4 rows a session, each a read of the same
-// pages, 33.5 and 30.1 us.
-constexpr int kShortPages = 64;
+// Taken for two rows a session on average and up to 128 pages a CTA, 64 and 32
+// for groups of 4 and 8, whose P V costs more.  Measured, this form against the
+// other (device time of a call; query / kv heads x dims):
+//   1 x 20 tokens, 8/8x64           2.7   12.1 us    64 x 300-900, 8/1x128        12.8  16.8 us
+//   4 x 300, 8/2x64                 4.6   10.4       8 x 500-1000, 32/4x128       12.9  16.0
+//   4 x 1500-2000, 32/8x128        11.6   19.4       2 x 900-1000, 64/8x64         6.9  14.3
+//   1 x 6000-8000, 32/8x128        19.9   22.0       1 x 12000-16000, 8/8x128     24.5  26.2
+//   64 x 500-1000, 32/8x128        46.2   52.5       64 x 1500-2000, 8/8x64       45.0  67.8
+//   256 x 400-900, 32/8x128       129.2  149.3       256 x 1200-1900, 8/4x128    132.6 143.5 (6.1 TB/s)
+// Past the rule the other wins: 64 x 1500-2000, 32/8x128: 89.5 and 85.7 us; 64 x
+// 3000-4000: 169 and 153 us; 256 x 100-900, 64/8x128: 142.8 and 137.3 us; 4 rows a
+// session, each a read of the same pages, 16 x 500-900: 39.6 and 23.8 us.
+constexpr int kShortPages = 128;
+constexpr int kShortCluster = 8;
 constexpr int kShortThreads = 256, kShortWarps = kShortThreads / 32;
 
 template <int D, int G>
@@ -883,10 +887,13 @@ __global__ void __launch_bounds__(kShortThreads, 2) window_short_kernel(const At
   __shared__ float scale[kShortWarps][8];                        // of what the warp holds, for a new maximum
   __shared__ float top[kShortWarps][8], sums[kShortWarps][8];
   __shared__ __align__(16) float part[kShortWarps][G][D];
+  __shared__ __align__(16) float joined[G][D];  // the CTA's, read by the cluster
+  __shared__ float joined_top[G], joined_sum[G];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, tq = lane & 3;
-  const int r = blockIdx.x, g = blockIdx.y;
+  const int C = (int)cluster_size(), rank = (int)cluster_rank(), r = blockIdx.x / C, g = blockIdx.y;
+  const int warps = kShortWarps * C, wid = kShortWarps * rank + warp;  // of the cluster
   griddep_wait();
-  if (r == 0 && g == 0 && tid == 0) *a.status = 0;
+  if (blockIdx.x == 0 && g == 0 && tid == 0) *a.status = 0;
   const int s = warp_find_session(a.b, r, lane);
   const int r0 = a.b.row_begin(s), n = a.b.row_begin(s + 1) - r0;
   if (r < r0 || r >= r0 + n) return;  // a row of no session
@@ -900,7 +907,7 @@ __global__ void __launch_bounds__(kShortThreads, 2) window_short_kernel(const At
   }
   auto logical = [&](int v) { return v < ns ? v : v + off; };
   // lane j: the page id of the warp's j-th page (-1: a hole)
-  const int mine = warp + kShortWarps * lane < np ? a.b.page(s, logical(warp + kShortWarps * lane)) : -1;
+  const int mine = wid + warps * lane < np ? a.b.page(s, logical(wid + warps * lane)) : -1;
   // the group's query rows as the second operand (heads past G: zeros)
   const size_t row = ((size_t)r * a.b.Hq + g * G) * D;
   uint4 qf[D / 32];
@@ -937,10 +944,10 @@ __global__ void __launch_bounds__(kShortThreads, 2) window_short_kernel(const At
   float acc[G][W] = {};
   int page = __shfl_sync(0xffffffffu, mine, 0);
   load_k(page);
-  load_v(page, logical(warp) * kPage);
-  for (int v = warp, j = 0; v < np; v += kShortWarps) {
+  load_v(page, logical(wid) * kPage);
+  for (int v = wid, j = 0; v < np; v += warps) {
     const int t0 = logical(v) * kPage, next = __shfl_sync(0xffffffffu, mine, ++j & 31);
-    const int t1 = logical(v + kShortWarps) * kPage;
+    const int t1 = logical(v + warps) * kPage;
     if (page < 0) {  // nothing to see: on to the next
       page = next;
       load_k(page);
@@ -1007,24 +1014,56 @@ __global__ void __launch_bounds__(kShortThreads, 2) window_short_kernel(const At
 #pragma unroll
     for (int i = 0; i < W; ++i) part[warp][h][lane * W + i] = acc[h][i];
   __syncthreads();
+  // the CTA's warps, then the cluster's CTAs: head h's maximum, sum and dims i, i + 1
   for (int i = 2 * tid; i < G * D; i += 2 * kShortThreads) {
-    const int h = i / D;
+    const int h = i / D, d = i % D;
     float mx = -INFINITY, sum = 0.f;
     float2 o = make_float2(0.f, 0.f);
+    auto add = [&](float t, float l1, float2 y) {
+      const float f = t == -INFINITY ? 0.f : ex2(t - mx);
+      sum += f * l1;
+      o.x += f * y.x;
+      o.y += f * y.y;
+    };
 #pragma unroll
     for (int w = 0; w < kShortWarps; ++w) mx = fmaxf(mx, top[w][h]);
 #pragma unroll
-    for (int w = 0; w < kShortWarps; ++w) {
-      const float f = top[w][h] == -INFINITY ? 0.f : ex2(top[w][h] - mx);
-      const float2 y = *reinterpret_cast<const float2*>(&part[w][h][i % D]);
-      sum += f * sums[w][h];
-      o.x += f * y.x;
-      o.y += f * y.y;
+    for (int w = 0; w < kShortWarps; ++w) add(top[w][h], sums[w][h], *reinterpret_cast<const float2*>(&part[w][h][d]));
+    if (C == 1) {
+      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      *reinterpret_cast<uint32_t*>(a.out + row + i) = pack_bf16x2(o.x * inv, o.y * inv);
+      if (a.lse && d == 0) a.lse[(size_t)r * a.b.Hq + g * G + h] = sum > 0.f ? (mx + lg2(sum)) * kLn2 : -INFINITY;
+    } else {
+      *reinterpret_cast<float2*>(&joined[h][d]) = o;
+      if (d == 0) joined_top[h] = mx, joined_sum[h] = sum;
+    }
+  }
+  if (C == 1) return;
+  __syncwarp();
+  cluster_sync();
+  for (int i = 2 * (tid + kShortThreads * rank); i < G * D; i += 2 * kShortThreads * C) {
+    const int h = i / D, d = i % D;
+    float t[kShortCluster], mx = -INFINITY, sum = 0.f;
+    float2 o = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int c = 0; c < kShortCluster; ++c) {
+      t[c] = c < C ? cluster_read(&joined_top[h], c) : -INFINITY;
+      mx = fmaxf(mx, t[c]);
+    }
+#pragma unroll
+    for (int c = 0; c < kShortCluster; ++c) {
+      if (t[c] == -INFINITY) continue;  // it saw nothing
+      const float f = ex2(t[c] - mx);
+      sum += f * cluster_read(&joined_sum[h], c);
+      o.x += f * cluster_read(&joined[h][d], c);
+      o.y += f * cluster_read(&joined[h][d + 1], c);
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     *reinterpret_cast<uint32_t*>(a.out + row + i) = pack_bf16x2(o.x * inv, o.y * inv);
-    if (a.lse && i % D == 0) a.lse[(size_t)r * a.b.Hq + g * G + h] = sum > 0.f ? (mx + lg2(sum)) * kLn2 : -INFINITY;
+    if (a.lse && d == 0) a.lse[(size_t)r * a.b.Hq + g * G + h] = sum > 0.f ? (mx + lg2(sum)) * kLn2 : -INFINITY;
   }
+  __syncwarp();
+  cluster_sync();  // no CTA leaves while another reads its results
 }
 
 // log2 of G (1, 2, 4, 8)
@@ -1035,7 +1074,7 @@ int log2_group(const pa_sessions& b) {
 
 struct Launch {
   int grid, slots, min_span, lanes, whole, device;
-  bool short_rows;  // the form for few rows over short caches
+  int cluster;  // > 0: the form for few rows over short caches, so many CTAs for each row and head
   size_t off_desc, off_lse, off_o, bytes;
 };
 
@@ -1066,7 +1105,15 @@ bool plan_launch(const pa_sessions& b, const Window& w, Launch* out) {
   if (spans > most) spans = most;
   if (spans < 1) spans = 1;
   out->grid = (int)spans * out->lanes;
-  out->short_rows = row_pages <= kShortPages && log2_group(b) <= 2 && b.num_rows <= 2 * b.n_sessions;
+  // the form for few rows over short caches, above: CTAs for a row until they
+  // cover the SMs twice or each warp has a page
+  out->cluster = 0;
+  if (b.num_rows <= 2 * b.n_sessions) {
+    int c = 1;
+    while (c < kShortCluster && row_pages > c * kShortWarps && (int64_t)b.num_rows * b.num_kv_heads * c <= sms) c *= 2;
+    const int lg = log2_group(b);
+    if (row_pages <= c * (lg == 0 ? kShortPages : 2 * kShortPages >> lg)) out->cluster = c;
+  }
   out->slots = (int)slots;
   out->off_desc = 256;
   out->off_lse = out->off_desc + ((size_t)out->grid * sizeof(Desc) + 255) / 256 * 256;
@@ -1101,18 +1148,22 @@ extern "C" pa_status pa_window_status(const void* d_workspace, void* stream, pa_
 namespace {
 
 template <int D, int G>
-bool launch_short(const pa::AttendArgs& a, const void* q, const void* k_pool, const void* v_pool, cudaStream_t cs) {
-  return pa_launch_early(pa::window_short_kernel<D, G>, dim3(a.b.rows, a.b.Hkv), dim3(pa::kShortThreads), 0, cs, 1, a,
+bool launch_short(const pa::AttendArgs& a, int cluster, const void* q, const void* k_pool, const void* v_pool,
+                  cudaStream_t cs) {
+  return pa_launch_early(pa::window_short_kernel<D, G>, dim3(a.b.rows * cluster, a.b.Hkv), dim3(pa::kShortThreads), 0, cs,
+                         cluster, a,
                          static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(k_pool),
                          static_cast<const uint16_t*>(v_pool));
 }
 
 template <int D>
-bool launch_short(const pa::AttendArgs& a, const void* q, const void* k_pool, const void* v_pool, cudaStream_t cs) {
+bool launch_short(const pa::AttendArgs& a, int cluster, const void* q, const void* k_pool, const void* v_pool,
+                  cudaStream_t cs) {
   switch (a.lg) {
-    case 0: return launch_short<D, 1>(a, q, k_pool, v_pool, cs);
-    case 1: return launch_short<D, 2>(a, q, k_pool, v_pool, cs);
-    default: return launch_short<D, 4>(a, q, k_pool, v_pool, cs);
+    case 0: return launch_short<D, 1>(a, cluster, q, k_pool, v_pool, cs);
+    case 1: return launch_short<D, 2>(a, cluster, q, k_pool, v_pool, cs);
+    case 2: return launch_short<D, 4>(a, cluster, q, k_pool, v_pool, cs);
+    default: return launch_short<D, 8>(a, cluster, q, k_pool, v_pool, cs);
   }
 }
 
@@ -1162,8 +1213,9 @@ extern "C" pa_status pa_window_attend(const pa_sessions* b, int32_t window, int3
   a.part_o = reinterpret_cast<float*>(ws + l.off_o);
   const int D = b->head_dim, G = 1 << a.lg;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (l.short_rows) {
-    const bool ok = D == 64 ? launch_short<64>(a, q, k_pool, v_pool, cs) : launch_short<128>(a, q, k_pool, v_pool, cs);
+  if (l.cluster > 0) {
+    const bool ok = D == 64 ? launch_short<64>(a, l.cluster, q, k_pool, v_pool, cs)
+                            : launch_short<128>(a, l.cluster, q, k_pool, v_pool, cs);
     return ok ? PA_OK : PA_ERR_CUDA;
   }
   CUtensorMap tq, tk, tv;

@@ -64,10 +64,10 @@ def test_attend_head_layouts(batch, heads):
     _attend_case(*BATCHES[batch], *heads, 130, 5, seed=3)
 
 
-# a table of more than 64 pages a session, or more than two rows of each, takes the
+# a table of more than 1024 pages a session, or more than two rows of each, takes the
 # form for long caches; the same rows with a narrow table the one for short ones
 @gpu
-@pytest.mark.parametrize("extra_pages", [1, 80])
+@pytest.mark.parametrize("extra_pages", [1, 1100])
 @pytest.mark.parametrize("heads", [(8, 8, 64), (4, 2, 128), (8, 2, 128), (16, 4, 64), (8, 1, 64)])
 @pytest.mark.parametrize("kv,rows,holes", [
     ([17, 33, 5, 300, 16], [1, 1, 1, 1, 1], ()),
@@ -86,6 +86,18 @@ def test_attend_short_windows_over_long_caches(window, sinks):
     kv, rows = [2000, 40, 1003, 17, 530], [2, 1, 2, 1, 2]
     _attend_case(kv, rows, 8, 2, 64, window, sinks, seed=8)
     _attend_case(kv, rows, 3, 3, 128, window, sinks, seed=9, holes=[(0, 0), (0, 124), (2, 40)])
+
+
+@gpu
+@pytest.mark.parametrize("heads", [(1, 1, 64), (2, 1, 128), (4, 1, 64), (16, 4, 128), (8, 1, 128), (64, 8, 64)])
+@pytest.mark.parametrize("kv,rows,holes", [
+    ([4000, 3], [1, 2], [(0, 0), (0, 100), (0, 249)]),
+    ([129, 0, 257], [1, 1, 1], ()),  # fewer pages than warps of a cluster, no keys
+    ([1000], [2], [(0, j) for j in range(8, 63)]),  # nothing but holes for most of a cluster's CTAs
+])
+def test_attend_clusters_share_a_row(kv, rows, holes, heads):
+    _attend_case(kv, rows, *heads, 0, 0, seed=16, holes=holes)
+    _attend_case(kv, rows, *heads, 777, 30, seed=17, holes=holes)
 
 
 @gpu
@@ -159,7 +171,7 @@ def test_attend_runs_alike_on_another_stream_and_twice(batch):
 
 @gpu
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("window,sinks,lo,hi,rows", [(700, 21, 900, 6000, 1), (0, 0, 500, 5000, 7), (300, 5, 400, 3000, 40)])
+@pytest.mark.parametrize("window,sinks,lo,hi,rows", [(700, 21, 900, 6000, 1), (2500, 21, 900, 6000, 1), (0, 0, 500, 5000, 7), (300, 5, 400, 3000, 40)])
 def test_attend_many_items_a_cta(window, sinks, lo, hi, rows, D):
     """Many short items in a row on every SM, whose blocks end inside pages: every run gives the same bits."""
     g = torch.Generator().manual_seed(13)
