@@ -815,7 +815,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the partial rows of the items that the spans cut: blocks (c, y) take the
 // item cut at the start of the span after CTA c's, when that is its first cut.
-// One warp per row, every kJoinY * 8-th of them; parts in the order of their keys.
+// A warp per row; when there are few rows and many parts the block's eight warps
+// per row, each every eighth part (the sum is kept in that order on every run).
 constexpr int kJoinY = 8;
 template <int D>
 __global__ void __launch_bounds__(256) window_join_kernel(const AttendArgs a) {
@@ -826,7 +827,9 @@ __global__ void __launch_bounds__(256) window_join_kernel(const AttendArgs a) {
   if (d.first != (int)blockIdx.x / a.lanes) return;
   const int in_lane = blockIdx.x % a.lanes;
   const int rows = d.n_tok << a.lg;  // tile 1 of a pair starts at row 128, token 128 / G
-  for (int prow = blockIdx.y * 8 + warp; prow < rows; prow += kJoinY * 8) {
+  __shared__ float part[8][D], part_sum[8];
+  const int team = rows <= 2 * kJoinY && d.last - d.first >= 16 ? 8 : 1, rank = team == 8 ? warp : 0;
+  for (int prow = (blockIdx.y * 8 + warp) / team; prow < rows; prow += kJoinY * 8 / team) {
     auto slot_of = [&](int c) { return (size_t)(c == d.first ? d.slot0 : 2 * (c * a.lanes + in_lane)) * 256 + prow; };
     float mx = -INFINITY;
     for (int c = d.first + lane; c <= d.last; c += 32) mx = fmaxf(mx, a.part_lse[slot_of(c)]);
@@ -834,12 +837,27 @@ __global__ void __launch_bounds__(256) window_join_kernel(const AttendArgs a) {
     for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     float sum = 0.f, acc[W] = {};
 #pragma unroll 4
-    for (int c = d.first; c <= d.last; ++c) {
+    for (int c = d.first + rank; c <= d.last; c += team) {
       const size_t at = slot_of(c);
       const float f = mx == -INFINITY ? 0.f : ex2(a.part_lse[at] - mx);
       sum += f;
 #pragma unroll
       for (int i = 0; i < W; ++i) acc[i] += f * a.part_o[at * D + lane * W + i];
+    }
+    if (team == 8) {  // all eight warps are at the same row
+#pragma unroll
+      for (int i = 0; i < W; ++i) part[warp][lane * W + i] = acc[i];
+      if (lane == 0) part_sum[warp] = sum;
+      __syncthreads();
+      if (warp == 0) {
+        for (int w = 1; w < 8; ++w) {
+          sum += part_sum[w];
+#pragma unroll
+          for (int i = 0; i < W; ++i) acc[i] += part[w][lane * W + i];
+        }
+      }
+      __syncthreads();
+      if (warp) continue;
     }
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     const size_t ro = (size_t)(d.row0 + (prow >> a.lg)) * a.b.Hq + (d.g << a.lg) + (prow & ((1 << a.lg) - 1));
