@@ -11,7 +11,7 @@
 //           through distributed shared memory (the scores' exponents are few, so
 //           8-bit digits made lanes collide; and one copy per four warps); then
 //           every warp counts what it keeps of its run, and with the counts before
-//           it writes the kept indices and scores in order.  Up to 1024 tokens,
+//           it writes the kept indices and scores in order.  Up to 512 tokens,
 //           one a thread, are ranked by comparing each with all
 //   gather  copies the kept K and V rows, in order, to the destination pages
 //
@@ -27,6 +27,7 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kRankMax = 512;  // most tokens of a row that are ranked by comparison
 constexpr int kGatherThreads = 256;
 constexpr int kKeysMax = 32768;  // keys that a CTA holds in shared memory (128 KB)
 constexpr int kBins = 2048, kCopies = 8;
@@ -41,7 +42,7 @@ struct EvictArgs {
   float* scores_out;
   int32_t *kept, *new_lens;
   int held_keys;  // keys that the launch's shared memory holds per CTA (0: none)
-  int small;      // no row has more than kSelThreads tokens
+  int small;      // no row has more than kRankMax tokens
 };
 
 // Order-preserving map of a score to an unsigned key: NaN above every number,
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     return;
   }
   const int lo = a.sinks, hi = n - a.recent, quota = a.budget - a.sinks - a.recent;
-  if (a.small) {  // one CTA, n <= 1024: thread t has token t
+  if (a.small) {  // one CTA, n <= kRankMax: thread t has token t
     const bool there = tid < n, mid = there && tid >= lo && tid < hi;
     const float f = there ? x[tid] : 0.f;
     // a token's place in the order (key, then the lower index); keys outside the
@@ -370,13 +371,17 @@ extern "C" pa_status pa_evict_tokens(const pa_sessions* b, const float* scores, 
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   const int64_t span = (int64_t)b->max_pages * pa::kPage;
   // CTAs per (session, kv head): more while SMs would be idle and a CTA would
-  // still have 4096 tokens, or until the keys fit shared memory
+  // still have 8192 tokens, or until the keys fit shared memory.  8 rows of 32768
+  // tokens: 1 CTA each 24 us, 2 20.9 us, 4 21.5 us, 8 33.9 us (a cluster of 8 such
+  // CTAs starts late); 8 rows of 16384: 1 18.4 us, 2 18.7 us, 4 21.0 us
   const int64_t longest = span < max_tokens ? span : max_tokens;
   const int64_t pairs = (int64_t)b->n_sessions * b->num_kv_heads;
   const pa_device dev = pa_current_device();
   int C = 1;
-  while (C < 8 && (longest / C > pa::kKeysMax || (pairs * C * 2 <= dev.sms && longest / (2 * C) >= 4096))) C *= 2;
-  a.small = longest <= pa::kSelThreads;
+  while (C < 8 && (longest / C > pa::kKeysMax || (C < 4 && pairs * C * 2 <= dev.sms && longest / (2 * C) >= 8192))) C *= 2;
+  // ranked by comparison against the radix selection, 4 sessions of 2 heads: 320
+  // tokens 6.1 and 8.9 us, 512 tokens 8.7 and 9.3 us, 640 tokens 10.9 and 9.1 us
+  a.small = longest <= pa::kRankMax;
   // (a warp's run is padded to 128 tokens)
   const int64_t per_cta = ((longest + C - 1) / C + 127) / 128 * 128 + 128 * pa::kSelWarps;
   constexpr int64_t most_held = pa::kKeysMax + 128 * pa::kSelWarps;

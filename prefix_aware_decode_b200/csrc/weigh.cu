@@ -582,12 +582,19 @@ pa_status launch(WeighArgs& a, const pa_sessions& b, const void* q, const void* 
     const int64_t seen = ((int64_t)a.w.window + b.num_rows + 14) / kPage + 1 + ((int64_t)a.w.sinks + 15) / kPage + 1;
     if (seen < pages) pages = seen;
   }
-  // K blocks in pairs halve the Q traffic; single ones when pairs would leave SMs idle
+  // K blocks in pairs halve the Q traffic; single ones when each of them can have
+  // an SM of its own: a chunk of 2000 rows, 8/8 heads of 64, over 2000 tokens (64
+  // pairs) 25 us in pairs, 16 us single; 512 rows, 32/8 heads of 128, over 4096
+  // tokens (128 pairs) 28.5 and 30.7 us, over 8192 tokens x 4 sessions 156 and
+  // 176 us; the decode step of 20000 tokens 13.6 and 17.3 us
   const int64_t pairs = (pages + 15) / 16 * b.num_kv_heads * b.n_sessions;
-  a.pair = pairs >= 2 * sms ? 2 : 1;
+  a.pair = 2 * pairs > sms ? 2 : 1;
   const int64_t line = (pages + 8 * a.pair - 1) / (8 * a.pair) * b.num_kv_heads * b.n_sessions;
   const int grid = (int)(line < sms ? line : sms);
-  // few rows: K streams (runs of items, the Q tile stays); many: Q streams
+  // few rows (one tile of columns a session): K streams (runs of items, the Q tile
+  // stays); many: Q streams.  8 sessions of 4000-8000, 32/8 heads of 128: 20 rows
+  // each 30.8 us with K streaming, 37.9 us with Q; 64 rows 53.6 and 54.0 us; 128
+  // rows 93.7 and 90.4 us; one session with 512 rows over 8192 tokens 74.5 and 55.9 us
   a.run = (int64_t)b.num_rows * G <= (int64_t)128 * b.n_sessions;
   a.nq = a.run ? 2 : Shape<D>::SLOTS - 2;  // 4 or 8 when not a.run: a multiple of the groups' turns
   a.nk = (Shape<D>::SLOTS - a.nq) / a.pair;
