@@ -37,10 +37,10 @@ def _lib_status(name, *args):
 # ------------------------------------------------------------------------------------------------ attention
 
 
-def _attend_case(kv, rows, Hq, Hkv, D, window, sinks, seed=0, holes=(), scale=0.0, extra_pages=1):
-    c = Cache(kv, rows, Hq, Hkv, D, seed=seed, holes=holes, extra_rows=2, extra_pages=extra_pages)
-    out = torch.full((c.n + 2, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
-    lse = torch.full((c.n + 2, Hq), 7.0, device="cuda")
+def _attend_case(kv, rows, Hq, Hkv, D, window, sinks, seed=0, holes=(), scale=0.0, extra_pages=1, extra_rows=2):
+    c = Cache(kv, rows, Hq, Hkv, D, seed=seed, holes=holes, extra_rows=extra_rows, extra_pages=extra_pages)
+    out = torch.full((c.n + extra_rows, Hq, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((c.n + extra_rows, Hq), 7.0, device="cuda")
     ref.run_attend(c, window, sinks, scale, out=out, lse=lse)
     o, l, tol, ltol = ref.attend(c, window, sinks, scale or None)
     ref.check(out[:c.n], o, tol, "out")
@@ -64,40 +64,41 @@ def test_attend_head_layouts(batch, heads):
     _attend_case(*BATCHES[batch], *heads, 130, 5, seed=3)
 
 
-# a table of more than 1024 pages a session, or more than two rows of each, takes the
-# form for long caches; the same rows with a narrow table the one for short ones
+# one or two rows a session over short caches have a form of their own; a table of more
+# than 1024 pages a session, or more rows, take the form for long caches
+FEW = {
+    "single": ([17, 33, 5, 300, 16], [1, 1, 1, 1, 1], (), 0),
+    "padded": ([17, 33, 5, 300, 16], [1, 1, 1, 1, 1], (), 2),
+    "none": ([1, 0, 64, 1, 990], [1, 1, 0, 1, 2], (), 0),  # rows without keys, a session without rows
+    "more": ([1, 0, 64, 3, 990, 31], [1, 2, 0, 9, 8, 4], (), 2),  # more rows than cached tokens
+    "holes": ([200, 150, 31], [1, 1, 1], [(0, 0), (0, 5), (1, 3), (1, 9), (0, 12), (2, 0), (2, 1)], 0),
+    "holes, more": ([200, 150, 31], [3, 7, 2], [(0, 0), (0, 5), (1, 3), (1, 9), (0, 12), (2, 0), (2, 1)], 0),
+    "long": ([4000, 3], [1, 1], [(0, 0), (0, 100), (0, 249)], 0),
+    "long, more": ([4000, 3], [5, 2], [(0, 0), (0, 100), (0, 249)], 1),
+    "fewer pages than warps": ([129, 0, 257], [1, 1, 1], (), 0),  # of a cluster
+    "mostly holes": ([1000], [2], [(0, j) for j in range(8, 63)], 0),  # nothing for some CTAs of a cluster
+}
+
+
 @gpu
 @pytest.mark.parametrize("extra_pages", [1, 1100])
-@pytest.mark.parametrize("heads", [(8, 8, 64), (4, 2, 128), (8, 2, 128), (16, 4, 64), (8, 1, 64)])
-@pytest.mark.parametrize("kv,rows,holes", [
-    ([17, 33, 5, 300, 16], [1, 1, 1, 1, 1], ()),
-    ([1, 0, 64, 1, 990], [1, 2, 0, 3, 2], ()),  # rows without keys, a session without rows
-    ([200, 150, 31], [1, 2, 1], [(0, 0), (0, 5), (1, 3), (1, 9), (0, 12), (2, 0), (2, 1)]),
-])
-def test_attend_short_and_long_tables(kv, rows, holes, heads, extra_pages):
-    _attend_case(kv, rows, *heads, 0, 0, seed=6, holes=holes, extra_pages=extra_pages)
-    _attend_case(kv, rows, *heads, 0, 0, seed=7, holes=holes, extra_pages=extra_pages, scale=0.7)
+@pytest.mark.parametrize("heads", [(1, 1, 64), (8, 8, 128), (4, 2, 128), (2, 1, 64), (8, 2, 128), (16, 4, 64), (8, 1, 64), (16, 2, 128)])
+@pytest.mark.parametrize("few", list(FEW))
+def test_attend_few_rows(few, heads, extra_pages):
+    kv, rows, holes, extra = FEW[few]
+    _attend_case(kv, rows, *heads, 0, 0, seed=6, holes=holes, extra_pages=extra_pages, extra_rows=extra)
+    _attend_case(kv, rows, *heads, 0, 0, seed=7, holes=holes, extra_pages=extra_pages, extra_rows=extra, scale=0.7)
 
 
 @gpu
-@pytest.mark.parametrize("window,sinks", [(1, 0), (15, 1), (16, 16), (17, 33), (500, 20), (975, 17), (976, 33)])
-def test_attend_short_windows_over_long_caches(window, sinks):
-    # up to 64 pages a row: the windows' edges inside pages, sinks that meet the window
-    kv, rows = [2000, 40, 1003, 17, 530], [2, 1, 2, 1, 2]
-    _attend_case(kv, rows, 8, 2, 64, window, sinks, seed=8)
-    _attend_case(kv, rows, 3, 3, 128, window, sinks, seed=9, holes=[(0, 0), (0, 124), (2, 40)])
-
-
-@gpu
-@pytest.mark.parametrize("heads", [(1, 1, 64), (2, 1, 128), (4, 1, 64), (16, 4, 128), (8, 1, 128), (64, 8, 64)])
-@pytest.mark.parametrize("kv,rows,holes", [
-    ([4000, 3], [1, 2], [(0, 0), (0, 100), (0, 249)]),
-    ([129, 0, 257], [1, 1, 1], ()),  # fewer pages than warps of a cluster, no keys
-    ([1000], [2], [(0, j) for j in range(8, 63)]),  # nothing but holes for most of a cluster's CTAs
-])
-def test_attend_clusters_share_a_row(kv, rows, holes, heads):
-    _attend_case(kv, rows, *heads, 0, 0, seed=16, holes=holes)
-    _attend_case(kv, rows, *heads, 777, 30, seed=17, holes=holes)
+@pytest.mark.parametrize("window,sinks", [(1, 0), (2, 3), (15, 1), (16, 16), (17, 33), (500, 20), (975, 17), (976, 33)])
+@pytest.mark.parametrize("rows", [[1, 1, 1, 1, 0], [2, 1, 4, 9, 3]])
+@pytest.mark.parametrize("heads", [(8, 2, 64), (3, 3, 128), (4, 2, 64), (8, 1, 128)])
+def test_attend_few_rows_under_windows(heads, rows, window, sinks):
+    # the windows' edges inside pages, sinks that meet the window, rows that see different pages
+    kv = [2000, 40, 1003, 17, 530]
+    _attend_case(kv, rows, *heads, window, sinks, seed=8, extra_rows=0)
+    _attend_case(kv, rows, *heads, window, sinks, seed=9, holes=[(0, 0), (0, 124), (2, 40)], extra_rows=1)
 
 
 @gpu
