@@ -445,15 +445,35 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Span& x = im.x;
       const int v0 = im.v0 + 8 * blk, rt0 = im.rt0, rt1 = im.rt1, p0 = x.p0, n = x.n;
       const bool there = v0 < x.np, q_new = im.q_new, q_last = im.q_last;
+      // who adds the item's sums to the scores: the group whose turn the only column
+      // tile is, else the block's first group; it asks for what it needs now
+      const bool single = rt1 - rt0 == 1, owner = single ? seq % of == mine : mine == 0;
+      // Nothing to add up: the barriers only (see below).  64 sessions of 2000-8000,
+      // 8/8 heads, dims 64: 99 -> 88 us, bound by these warps' steps per item; with
+      // dims 128, bound by memory, the shorter way made it slower (231 -> 247 us for
+      // 64 sessions of 2000-20000): the warps then poll beside the loaders.
+      if (D == 64 && a.run && single && !owner) {
+        if (q_new) {
+          qcur = qr;
+          qr.next(a.nq);
+        }
+        if (!(ok = wwait(mi.qfull[qcur.slot], qcur.phase, 11))) break;
+        ++seq;
+        __syncwarp();
+        if (lane == 0) {
+          if (q_last) mbar_arrive(bar(mi.qempty[qcur.slot]));
+          mbar_arrive(bar(mi.comb[e]));
+          mbar_arrive(bar(mi.it_empty[e]));
+        }
+        ++it;
+        continue;
+      }
       const int v1 = min(v0 + 8, x.np);
       const int t = x.page_index(v0 + (key >> 4)) * kPage + (key & 15);  // this thread's token
       const int t_first = x.page_index(v0) * kPage, t_last = x.page_index(max(v1 - 1, 0)) * kPage + kPage - 1;
       // rows that see token t: indices [i0, i1)
       const bool always = a.w.window == 0 || t < a.w.sinks;
       const int i0 = max(0, t - p0), i1 = always ? n : (int)min((long long)n, (long long)t + a.w.window - p0);
-      // who adds the item's sums to the scores: the group whose turn the only column
-      // tile is, else the block's first group; it asks for what it needs now
-      const bool single = rt1 - rt0 == 1, owner = single ? seq % of == mine : mine == 0;
       const bool writes = owner && v0 + (key >> 4) < x.np && t < x.kv && t < a.max_tokens;
       float* score = a.scores + ((size_t)im.s * a.b.Hkv + im.g) * a.max_tokens + t;
       float old = 0.f;
