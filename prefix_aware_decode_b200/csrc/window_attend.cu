@@ -138,19 +138,6 @@ struct Item {
   int part;  // partial slot, -1: the whole item
 };
 
-template <int D>
-struct Shape {
-  static constexpr int HALVES = D / 64;
-  static constexpr int BLK = 128 * 128;               // 128 rows x 64 dims
-  static constexpr int TILE = HALVES * BLK;           // a Q tile, a K block, a V block
-  static constexpr int NS = D == 128 ? 5 : 8;         // ring slots
-  static constexpr int OFF_Q = 0, OFF_RING = 2 * TILE, OFF_MISC = OFF_RING + NS * TILE;
-  static constexpr int MISC = 3072;
-  static constexpr int SMEM = OFF_MISC + MISC;
-  static constexpr uint32_t T_S = 0, T_O = 256;       // TMEM columns: S0, S1, O0, O1
-};
-static_assert(Shape<128>::SMEM <= 232448 && Shape<64>::SMEM <= 232448, "shared memory");
-
 struct Misc {
   uint64_t full[8], empty[8];          // ring
   uint64_t q_full, q_empty, o_free, joined, done;
@@ -161,7 +148,18 @@ struct Misc {
   Item items[kQueue];
   float2 exch[2][128];                 // (m, l) of the two groups
 };
-static_assert(sizeof(Misc) <= 3072, "shared memory");
+
+template <int D>
+struct Shape {
+  static constexpr int HALVES = D / 64;
+  static constexpr int BLK = 128 * 128;               // 128 rows x 64 dims
+  static constexpr int TILE = HALVES * BLK;           // a Q tile, a K block, a V block
+  static constexpr int NS = D == 128 ? 5 : 8;         // ring slots
+  static constexpr int OFF_Q = 0, OFF_RING = 2 * TILE, OFF_MISC = OFF_RING + NS * TILE;
+  static constexpr int SMEM = OFF_MISC + (int)sizeof(Misc);
+  static constexpr uint32_t T_S = 0, T_O = 256;       // TMEM columns: S0, S1, O0, O1
+};
+static_assert(Shape<128>::SMEM <= 232448 && Shape<64>::SMEM <= 232448, "shared memory");
 
 // What a CTA finds its span with (aliases the ring before any load): sums of
 // kThreads slots' blocks, per chunk, and a copy of the sessions' rows and
