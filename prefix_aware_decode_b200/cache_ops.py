@@ -81,7 +81,8 @@ def window_attend(q, k_pool, v_pool, block_table, kv_lens, cu_rows, *, window: i
     t when t <= p and (window == 0 or t > p - window or t < sinks).
 
     q bf16 [rows][Hq][D]; pools bf16 [num_pages][Hkv][P][D].  Returns (out bf16
-    [rows][Hq][D], lse fp32 [rows][Hq]); rows that see nothing get 0 and -inf.
+    [rows][Hq][D], lse fp32 [rows][Hq]); rows that see nothing get 0 and -inf, rows
+    of no session are not written (undefined in tensors that the call allocates).
     `workspace` (window_workspace) is allocated by the call when not given.
     """
     if stream is not None:
