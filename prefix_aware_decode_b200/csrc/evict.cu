@@ -16,7 +16,9 @@
 //   gather  copies the kept K and V rows, in order, to the destination pages
 //
 // The selection reads the scores once; the gather, which moves the bytes, is
-// bound by memory.
+// bound by memory.  Measured, 16 sessions of 20000-32768 tokens, 8 heads of 128, to
+// 4096: selection 34 us, bound by the ALU and shared memory work of its passes;
+// gather 92 us for 0.5 GB (5.5 TB/s); the call 127 us.
 #include <type_traits>
 
 #include "ptx.cuh"
