@@ -41,7 +41,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kThreads = 640;
 constexpr int kGroups = 1024;  // entries of the table of item prefixes
 constexpr int kQueue = 4;      // entries of the CTA's item queue
-constexpr int kFmaPairs = 4;   // of 16 pairs of scores: exponentials on the FMA pipe
+// Of 16 pairs of scores: exponentials on the FMA pipe.  Prompt chunks (above) with
+// 0, 3, 4, 6: 451, 406, 404, 435 us.
+constexpr int kFmaPairs = 4;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 // First failure of a device-side wait since pa_weigh_status last read it.
