@@ -904,8 +904,8 @@ __global__ void __launch_bounds__(256) window_join_kernel(const AttendArgs a) {
 //   4 x 300, 8/2x64                 4.6   10.4       8 x 500-1000, 32/4x128       12.9  16.0
 //   4 x 1500-2000, 32/8x128        11.6   19.4       2 x 900-1000, 64/8x64         6.9  14.3
 //   1 x 6000-8000, 32/8x128        19.9   22.0       1 x 12000-16000, 8/8x128     24.5  26.2
-//   64 x 500-1000, 32/8x128        46.2   52.5       64 x 1500-2000, 8/8x64       45.0  67.8
-//   256 x 400-900, 32/8x128       129.2  149.3       256 x 1200-1900, 8/4x128    132.6 143.5 (6.1 TB/s)
+//   64 x 500-1000, 32/8x128        44.4   52.5       64 x 1500-2000, 8/8x64       45.0  67.8
+//   256 x 400-900, 32/8x128       124.3  149.3       256 x 1200-1900, 8/4x128    132.6 143.5 (6.1 TB/s)
 // Past the rule the other wins: 64 x 1500-2000, 32/8x128: 89.5 and 85.7 us; 64 x
 // 3000-4000: 169 and 153 us; 256 x 100-900, 64/8x128: 142.8 and 137.3 us; 4 rows a
 // session, each a read of the same pages, 16 x 500-900: 39.6 and 23.8 us.
@@ -914,9 +914,9 @@ constexpr int kShortCluster = 8;
 constexpr int kShortThreads = 256, kShortWarps = kShortThreads / 32;
 
 template <int D, int G>
-__global__ void __launch_bounds__(kShortThreads, 2) window_short_kernel(const AttendArgs a, const uint16_t* __restrict__ q,
-                                                                        const uint16_t* __restrict__ k_pool,
-                                                                        const uint16_t* __restrict__ v_pool) {
+__global__ void __launch_bounds__(kShortThreads, 2) window_short_kernel(const AttendArgs a, const uint16_t* q,
+                                                                        const uint16_t* k_pool,
+                                                                        const uint16_t* v_pool) {
   constexpr int W = D / 32;  // dims of a lane in P V
   __shared__ __align__(16) float weight[kShortWarps][kPage][G];  // of the warp's page
   __shared__ float scale[kShortWarps][8];                        // of what the warp holds, for a new maximum
@@ -948,16 +948,17 @@ __global__ void __launch_bounds__(kShortThreads, 2) window_short_kernel(const At
   uint4 qf[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
-    qf[i] = gr < G ? __ldg(reinterpret_cast<const uint4*>(q + row + gr * D + 32 * i + 8 * tq)) : make_uint4(0, 0, 0, 0);
+    qf[i] = gr < G ? *reinterpret_cast<const uint4*>(q + row + gr * D + 32 * i + 8 * tq) : make_uint4(0, 0, 0, 0);
   uint4 k0[D / 32], k1[D / 32];  // rows gr and gr + 8 of the page's keys
   uint32_t raw[kPage][W / 2];    // its V rows; those that the row does not see are not read
+  // (plain loads: the kernel before this one may still be filling the pages when it starts)
   auto load_k = [&](int page) {
     if (page < 0) return;
     const uint16_t* k = k_pool + (((size_t)page * a.b.Hkv + g) * kPage + gr) * D + 8 * tq;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-      k0[i] = __ldg(reinterpret_cast<const uint4*>(k + 32 * i));
-      k1[i] = __ldg(reinterpret_cast<const uint4*>(k + 8 * D + 32 * i));
+      k0[i] = *reinterpret_cast<const uint4*>(k + 32 * i);
+      k1[i] = *reinterpret_cast<const uint4*>(k + 8 * D + 32 * i);
     }
   };
   auto load_v = [&](int page, int t0) {
@@ -967,9 +968,9 @@ __global__ void __launch_bounds__(kShortThreads, 2) window_short_kernel(const At
     for (int key = 0; key < kPage; ++key) {
       const bool see = a.w.sees(p, t0 + key);
       if (W == 2) {
-        raw[key][0] = see ? __ldg(reinterpret_cast<const uint32_t*>(vp + key * D)) : 0u;
+        raw[key][0] = see ? *reinterpret_cast<const uint32_t*>(vp + key * D) : 0u;
       } else {
-        const uint2 y = see ? __ldg(reinterpret_cast<const uint2*>(vp + key * D)) : make_uint2(0u, 0u);
+        const uint2 y = see ? *reinterpret_cast<const uint2*>(vp + key * D) : make_uint2(0u, 0u);
         raw[key][0] = y.x;
         raw[key][W / 2 - 1] = y.y;
       }
