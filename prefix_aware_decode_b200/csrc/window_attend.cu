@@ -25,19 +25,33 @@
 //
 // Roles (384 threads): warps 0-3 and 4-7 softmax groups, one thread per row;
 // warp 8 issues the products; warp 9 walks the items and loads (TMA).  Per
-// block and tile: S = Q K^T (TMEM), P = exp2(S c - m c) rounded to bf16 (half a
-// step, 2^-8 of a weight, averaged over the keys; l sums the unrounded weights)
-// written over S, O += P V (TMEM).  The running maximum is raised, and O
-// rescaled, only when it grows by more than 2^8: numerator and denominator use
-// the same maximum, so the result is unchanged.
+// block and tile: S = Q K^T (TMEM), P = exp2(S c - m c) written over S as P_hi + P_lo,
+// O += P V (TMEM).  P_hi is P cut to bf16, so that P - P_hi is exact in fp32, P_lo that
+// rest rounded to bf16: together within 2^-16 of P, as the planned decode's weights (one
+// bf16 alone is off by up to 2^-8 of a weight and left outputs 0.8 % off); l sums P.
+//   items of at most 64 rows   each row has two lanes of the tile (Q is loaded to both),
+//     16 rows to a warp's 32 lanes: one lane writes P_hi, the other P_lo, one product
+//     serves both and the epilogue adds the two
+//   more rows                  two products, P_hi V and P_lo V
+// The running maximum is raised, and O rescaled, only when it grows by more than 2^8:
+// numerator and denominator use the same maximum, so the result is unchanged.
+//
+// Measured, with one bf16 | two products throughout | as it is: 64 windowed decodes 184,
+// 231, 195 us, a prompt chunk 2.0, 2.8, 2.75 ms, windowed chunks 42, 56, 51 us.  A block's
+// weights are handed over at once: P_hi first (in 1, 2 or 4 parts) and P_lo while its
+// product runs: prompt chunk 2.8, 2.85, 3.4 ms, windowed chunks 54, 56, 65 us, for with
+// two tiles the product warp then waits where it could serve the other tile.
 //
 // Bounds and measured device times, 32/8 heads of 128: decode rows by the bytes of
-// the visible cache (64 sessions, window 4096: 1.08 GB in 180 us, 6.0 TB/s; two of
-// 100001-131072: 0.98 GB in 155 us, 6.3 TB/s); a prompt chunk of 4096 rows over
+// the visible cache and by how long a block's slots are held through its softmax (64
+// sessions, window 4096: 1.08 GB in 195 us captured back to back, 222 us issued one by
+// one; two of 100001-131072: 0.98 GB in 165-180 us); a prompt chunk of 4096 rows over
 // 32768 tokens by the chain scores - softmax - product of a tile, two tiles being
-// all that tensor memory holds at 128 dims, and by power (1.77 ms alone, 1.16
-// PFLOP/s, 1.99 ms in a loop; tensor and exponential pipes 62% busy); a call of one
-// short item by its steps, about 11 us.
+// all that tensor memory holds at 128 dims, and by power (2.45-2.85 ms, 0.72-0.84
+// PFLOP/s for the 1.5 times as many that the two parts of the weights take); a call of
+// one short item by its steps, about 11 us.
+#include <type_traits>
+
 #include "ptx.cuh"
 #include "sessions.cuh"
 #include "tmap.h"
@@ -51,16 +65,13 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kThreads = 384;
 constexpr int kMaxChunks = 256;      // chunks of kThreads tile slots that a CTA sums
 constexpr int kQueue = 2;            // entries of the CTA's item queue
-// parts of a block's weights that are handed over one by one.  In 1, 2, 4 parts: a
-// prompt chunk 2.03, 1.98, 2.09 ms, windowed decode 176, 179, 185 us, windowed chunks
-// 42.7, 43.2, 47.4 us
-constexpr int kParts = 2;
 // items of at most so many blocks are not cut: 8 windowed chunks of 1-700 rows 42 us,
 // all items cut 50 us; whole up to 32 blocks: 4 sessions of 4096, 3 rows, 38 and 26 us
 constexpr int kWholeBlocks = 8;
 // most kv heads walked side by side (148 SMs = 37 spans of 4); 1: 64 windowed decodes
 // 183.6 and 179.8 us, 64 of 300-1000 with 5 rows 58.8 and 52.9 us
 constexpr int kLanes = 4;
+constexpr int kTwinRows = 64;        // most rows of an item that has each in two lanes
 constexpr float kRaise = 8.f;        // log2 growth of a maximum that raises it
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
@@ -156,7 +167,7 @@ struct Item {
 struct Misc {
   uint64_t full[8], empty[8];          // ring
   uint64_t q_full, q_empty, o_free, joined, done;
-  uint64_t s_full[2], p_full[2][kParts], o_full[2];  // p_full: by tile and part of the block's keys
+  uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t it_full[kQueue], it_empty[kQueue];
   uint32_t tmem;
   int fail;
@@ -193,7 +204,8 @@ static_assert(sizeof(Sums) <= 5 * Shape<64>::TILE, "ring");
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     window_attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap tq,
-                         const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
+                         const __grid_constant__ CUtensorMap tq16, const __grid_constant__ CUtensorMap tk,
+                         const __grid_constant__ CUtensorMap tv) {
   using S = Shape<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023) {  // the swizzle needs it; the kernel has no other shared memory before it
@@ -222,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(mi.done), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(mi.s_full[i]), 1);
-      for (int c = 0; c < kParts; ++c) mbar_init(bar(mi.p_full[i][c]), 4);
+      mbar_init(bar(mi.p_full[i]), 4);
       mbar_init(bar(mi.o_full[i]), 1);
     }
     for (int i = 0; i < kQueue; ++i) {
@@ -234,6 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 9 && lane == 0) {
     prefetch_tmap(&tq);
+    prefetch_tmap(&tq16);
     prefetch_tmap(&tk);
     prefetch_tmap(&tv);
   }
@@ -398,9 +411,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(bar(mi.it_full[e]));
       }
       if (it > 0 && !wwait(mi.q_empty, it - 1, 2)) break;
-      const bool pair = (t.n_tok << a.lg) > 128;
+      const int rows = t.n_tok << a.lg;
+      const bool pair = rows > 128;
       ++n_q;
-      if (lead) {
+      if (lead && rows <= kTwinRows) {  // 16 rows to lanes 32 i .. 32 i + 15 of the tile, and again to the 16 after them
+        const int n16 = (rows + 15) >> 4;
+        mbar_arrive_expect_tx(bar(mi.q_full), n16 * 2 * S::HALVES * 2048);
+        for (int i = 0; i < n16; ++i)
+#pragma unroll
+          for (int h = 0; h < 2 * S::HALVES; ++h)
+            tma_load_3d(smem_u32(smem + S::OFF_Q + (h >> 1) * S::BLK + (2 * i + (h & 1)) * 2048), &tq16, 64 * (h >> 1),
+                        g << a.lg, t.r0 + i * (16 >> a.lg), bar(mi.q_full));
+      } else if (lead) {
         mbar_arrive_expect_tx(bar(mi.q_full), (pair ? 2 : 1) * S::TILE);
         for (int i = 0; i < (pair ? 2 : 1); ++i)
 #pragma unroll
@@ -477,27 +499,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     };
-    // O += P V, V in ring slot sl, part by part as the weights are written
-    auto issue_o = [&](int tile, int sl, int pages, bool first, int phase) -> bool {
+    // O += P V, V in ring slot sl
+    auto issue_o = [&](int tile, int sl, int pages, bool first, bool twin) {
+      tc_fence_after();
       const uint32_t va = ring_lo + sl * (S::TILE >> 4), d = tm + S::T_O + tile * D, p = tm + S::T_S + tile * 128;
-#pragma unroll
-      for (int part = 0; part < kParts; ++part) {
-        if (part > 0 && !wwait(mi.p_full[tile][part], phase, 18)) return false;
-        tc_fence_after();
-        auto pv = [&](int c) {
-          umma_bf16_ts(d, p + 8 * c, sdesc_sw128_lo(va + c * 128, S::BLK >> 4, 64), idesc_o, first && c == 0 ? 0u : 1u);
-        };
-        if (lead) {
-          if (pages == 8) {
-#pragma unroll
-            for (int c = 8 / kParts * part; c < 8 / kParts * (part + 1); ++c) pv(c);
-          } else {
-            for (int c = 8 / kParts * part; c < min(pages, 8 / kParts * (part + 1)); ++c) pv(c);
-          }
+      auto pv = [&](int c) {
+        const uint64_t v = sdesc_sw128_lo(va + c * 128, S::BLK >> 4, 64);
+        if (twin) {
+          umma_bf16_ts(d, p + 8 * c, v, idesc_o, first && c == 0 ? 0u : 1u);
+        } else {
+          umma_bf16_ts(d, p + 16 * c, v, idesc_o, first && c == 0 ? 0u : 1u);
+          umma_bf16_ts(d, p + 16 * c + 8, v, idesc_o, 1u);
         }
-        __syncwarp();
+      };
+      if (lead) {
+        if (pages == 8) {
+#pragma unroll
+          for (int c = 0; c < 8; ++c) pv(c);
+        } else {
+          for (int c = 0; c < pages; ++c) pv(c);
+        }
       }
-      return true;
+      __syncwarp();
     };
     auto commit = [&](uint64_t& b) {
       if (lead) umma_commit(bar(b));
@@ -509,7 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wwait(mi.it_full[e], it / kQueue, 5)) break;
       const Item& x = mi.items[e];
       const int b1 = uni(x.b1), jb = uni(x.b0), n = b1 - jb, np = uni(x.t.np);
-      const bool pair = (uni(x.t.n_tok) << a.lg) > 128;
+      const int rows = uni(x.t.n_tok) << a.lg;
+      const bool pair = rows > 128, twin = rows <= kTwinRows;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(mi.it_empty[e]));
       if (b1 < 0) break;
@@ -528,18 +552,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           // (what does not depend on the weights is waited for first: the way from a
           // tile's last weights to its next scores is what a block costs)
           ok = wait_load(pv) && (!more || wait_load(pk)) && (j || it == 0 || wwait(mi.o_free, it - 1, 9)) &&
-               wwait(mi.p_full[0][0], c0, 8) && issue_o(0, pv % S::NS, pages, j == 0, c0);
+               wwait(mi.p_full[0], c0, 8);
           if (!ok) break;
           ++c0;
+          issue_o(0, pv % S::NS, pages, j == 0, false);
           if (more) {
             issue_s(0, 0, pk % S::NS);
           } else {
             commit(mi.o_full[0]);
           }
           // tile 1, which frees the slots
-          ok = wwait(mi.p_full[1][0], c1, 8) && issue_o(1, pv % S::NS, pages, j == 0, c1);
-          if (!ok) break;
+          if (!(ok = wwait(mi.p_full[1], c1, 8))) break;
           ++c1;
+          issue_o(1, pv % S::NS, pages, j == 0, false);
           if (more) {
             issue_s(1, 1, pk % S::NS);
             commit(mi.empty[pv % S::NS]);
@@ -563,9 +588,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int phase = tile ? c1++ : c0++;
           const bool more = j + 2 < n;
           const int pk = pos_k(base, j + 2);
-          ok = wait_load(pv) && (j || it == 0 || wwait(mi.o_free, it - 1, 11)) && wwait(mi.p_full[tile][0], phase, 10) &&
-               issue_o(tile, pv % S::NS, pages, j < 2, phase) && (!more || wait_load(pk));
+          ok = wait_load(pv) && (j || it == 0 || wwait(mi.o_free, it - 1, 11)) && wwait(mi.p_full[tile], phase, 10);
           if (!ok) break;
+          issue_o(tile, pv % S::NS, pages, j < 2, twin);
+          if (more && !(ok = wait_load(pk))) break;
           if (more) {
             issue_s(tile, 0, pk % S::NS);
             commit(mi.empty[pv % S::NS]);
@@ -601,9 +627,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(bar(mi.it_empty[e]));
       if (b1 < 0) break;
       const int n = b1 - b0;
-      const bool pair = (t.n_tok << a.lg) > 128;
+      const bool pair = (t.n_tok << a.lg) > 128, twin = t.n_tok << a.lg <= kTwinRows;
+      const bool low = twin && (lane & 16);              // this thread writes P_lo of its row
+      const int trow = twin ? quad * 16 + (lane & 15) : row;  // row of the tile
       const int tok0 = pair ? grp << (7 - a.lg) : 0;     // first token of this group's tile
-      const int tok = tok0 + (row >> a.lg);              // this row's token
+      const int tok = tok0 + (trow >> a.lg);             // this row's token
       const int p = t.p0 + min(tok, t.n_tok - 1);        // rows past the tile repeat its last
       const int p_min = t.p0 + tok0, p_max = t.p0 + min(tok0 + (128 >> a.lg), t.n_tok) - 1;
       const int kv_end = a.b.kv_len(t.s), seen_from = a.w.first(max(t.p0, 0));
@@ -656,14 +684,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             float z[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) z[i] = 0.f;
-            tmem_st32(t_s, z);
-            tmem_st32(t_s + 32, z);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_st32(t_s + 32 * c, z);
             tmem_wait_st();
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0)
-            for (int i = 0; i < kParts; ++i) mbar_arrive(bar(mi.p_full[grp][i]));
+          if (lane == 0) mbar_arrive(bar(mi.p_full[grp]));
           continue;
         }
         float x[4][32];
@@ -677,9 +704,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int t0 = t.page_index(v0 + pg) * kPage;
             const bool gone = pg >= pages || (holes >> pg & 1);
             // bit i: this row sees token t0 + i
-            const int top = p - t0, low = a.w.window ? p - a.w.window - t0 : -1, sk = a.w.sinks - t0;
+            const int top = p - t0, under = a.w.window ? p - a.w.window - t0 : -1, sk = a.w.sinks - t0;
             const uint32_t upto = top < 0 ? 0u : 0xffffu >> (15 - min(top, 15));
-            const uint32_t from = low < 0 ? 0xffffu : 0xffffu << min(low + 1, 16);
+            const uint32_t from = under < 0 ? 0xffffu : 0xffffu << min(under + 1, 16);
             const uint32_t sink = sk <= 0 ? 0u : 0xffffu >> (16 - min(sk, 16));
             const uint32_t see = gone ? 0u : upto & (from | sink);
             if (__any_sync(0xffffffffu, see != 0xffffu)) {
@@ -699,6 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 1; i < 31; i += 2) mq[c] = max3(mq[c], x[c][i], x[c][i + 1]);
         }
         float mx = max3(max3(mq[0], mq[1], x[0][31]), max3(mq[2], mq[3], x[1][31]), fmaxf(x[2][31], x[3][31]));
+        if (twin) mx = __shfl_sync(0xffffffffu, mx, lane & 15);  // both lanes of a row rescale alike
         mx *= a.scale_log2;
         if (first) {
           m = mx;
@@ -715,25 +743,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float mc = m == -INFINITY ? 0.f : -m;
         const float2 sc = make_float2(a.scale_log2, a.scale_log2), mm = make_float2(mc, mc);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // the weights, 32 keys (16 words of two) at a time
+        // the weights, 32 keys at a time
+        auto cut = [](float2 y) {  // to bf16
+          return make_float2(__uint_as_float(__float_as_uint(y.x) & 0xffff0000u),
+                             __uint_as_float(__float_as_uint(y.y) & 0xffff0000u));
+        };
+        const float2 neg = make_float2(-1.f, -1.f);
+        // of a row in two lanes: y cut, or what that leaves
+        const float2 fy = low ? make_float2(1.f, 1.f) : make_float2(0.f, 0.f), fc = low ? neg : make_float2(1.f, 1.f);
+        auto weights = [&](auto twin_tag) {
+          constexpr bool TWIN = decltype(twin_tag)::value;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float pw[32];
+          for (int c = 0; c < 4; ++c) {
+            float pw[32];
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float2 z = ffma2(make_float2(x[c][i], x[c][i + 1]), sc, mm);
-            const float2 y = make_float2(ex2(z.x), ex2(z.y));
-            sum[(i >> 1) & 1] = fadd2(sum[(i >> 1) & 1], y);
-            pw[i >> 1] = __uint_as_float(pack_bf16x2(y.x, y.y));
+            for (int i = 0; i < 32; i += 2) {
+              const float2 z = ffma2(make_float2(x[c][i], x[c][i + 1]), sc, mm);
+              const float2 y = make_float2(ex2(z.x), ex2(z.y));
+              sum[(i >> 1) & 1] = fadd2(sum[(i >> 1) & 1], y);
+              if (TWIN) {
+                const float2 v = ffma2(cut(y), fc, fmul2(y, fy));
+                pw[i >> 1] = __uint_as_float(pack_bf16x2(v.x, v.y));
+              } else {  // of 16 keys 8 words P_hi, 8 words P_lo
+                const float2 v = ffma2(cut(y), neg, y);
+                const int w = (i & 16) + ((i & 15) >> 1);
+                pw[w] = __uint_as_float(__byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x7632));
+                pw[w + 8] = __uint_as_float(pack_bf16x2(v.x, v.y));
+              }
+            }
+            if (TWIN) tmem_st16<0>(t_s + 16 * c, pw);
+            else tmem_st32(t_s + 32 * c, pw);
           }
-          tmem_st16<0>(t_s + 16 * c, pw);
-          if ((c + 1) % (4 / kParts) == 0) {
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(mi.p_full[grp][(c + 1) / (4 / kParts) - 1]));
-          }
-        }
+        };
+        if (twin) weights(std::true_type{});
+        else weights(std::false_type{});
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(mi.p_full[grp]));
         l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
       }
       if (!ok) break;
@@ -768,9 +815,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         two = n > 1;
       }
       const bool have = n_mine > 0;  // this group's accumulator was written
-      const bool live = tok < t.n_tok;
-      const int r = t.r0 + tok, h = (g << a.lg) + (row & ((1 << a.lg) - 1));
-      const int prow = (pair ? grp * 128 : 0) + row;
+      const bool live = tok < t.n_tok && !low;
+      const int r = t.r0 + tok, h = (g << a.lg) + (trow & ((1 << a.lg) - 1));
+      const int prow = (pair ? grp * 128 : 0) + trow;
 #pragma unroll 1
       for (int c = d0; c < d0 + dn; c += 32) {
         float o[32];
@@ -786,6 +833,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld_into(o1);
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] += o1[i] * w1;
+        }
+        if (twin) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] += __shfl_xor_sync(0xffffffffu, o[i], 16);
         }
         if (live) {
           if (part < 0) {
@@ -1204,13 +1255,13 @@ bool launch_short(const pa::AttendArgs& a, int cluster, const void* q, const voi
 }
 
 template <int D>
-bool launch(const pa::AttendArgs& a, const pa::Launch& l, const CUtensorMap& tq, const CUtensorMap& tk,
-            const CUtensorMap& tv, cudaStream_t cs) {
+bool launch(const pa::AttendArgs& a, const pa::Launch& l, const CUtensorMap& tq, const CUtensorMap& tq16,
+            const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t cs) {
   auto* k = pa::window_attend_kernel<D>;
   constexpr int smem = pa::Shape<D>::SMEM;
   static std::atomic<uint64_t> allowed{0};
   if (!pa_allow_smem(k, smem, l.device, allowed)) return false;
-  if (!pa_launch_early(k, dim3(l.grid), dim3(pa::kThreads), smem, cs, 1, a, tq, tk, tv)) return false;
+  if (!pa_launch_early(k, dim3(l.grid), dim3(pa::kThreads), smem, cs, 1, a, tq, tq16, tk, tv)) return false;
   if (l.grid == l.lanes || a.whole) return true;  // no item is cut
   return pa_launch_early(pa::window_join_kernel<D>, dim3(l.grid - l.lanes, pa::kJoinY), dim3(256), 0, cs, 1, a);
 }
@@ -1254,10 +1305,11 @@ extern "C" pa_status pa_window_attend(const pa_sessions* b, int32_t window, int3
                             : launch_short<128>(a, l.cluster, q, k_pool, v_pool, cs);
     return ok ? PA_OK : PA_ERR_CUDA;
   }
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tq16, tk, tv;
   if (!pa::tmap_q(&tq, q, b->num_rows, b->num_q_heads, D, G, 128 / G) ||
+      !pa::tmap_q(&tq16, q, b->num_rows, b->num_q_heads, D, G, 16 / G) ||
       !pa::tmap_pool(&tk, k_pool, b->num_pages_in_pool, b->num_kv_heads, D) ||
       !pa::tmap_pool(&tv, v_pool, b->num_pages_in_pool, b->num_kv_heads, D))
     return PA_ERR_CUDA;
-  return (D == 64 ? launch<64>(a, l, tq, tk, tv, cs) : launch<128>(a, l, tq, tk, tv, cs)) ? PA_OK : PA_ERR_CUDA;
+  return (D == 64 ? launch<64>(a, l, tq, tq16, tk, tv, cs) : launch<128>(a, l, tq, tq16, tk, tv, cs)) ? PA_OK : PA_ERR_CUDA;
 }

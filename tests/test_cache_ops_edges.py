@@ -1,0 +1,69 @@
+"""Session-cache operators at their edges: the precision of the attention weights,
+what no element-wise bound over random values shows, and inputs that are not
+finite, not there or not allowed."""
+import math
+
+import pytest
+import torch
+
+import cache_ref as ref
+from cache_ref import Cache
+
+gpu = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------------------------------ precision
+
+
+def _attend(c, window=0, sinks=0, scale=None):
+    """out in 64 bits, and the bound for weights kept to about 16 bits."""
+    scale = scale or 1 / math.sqrt(c.D)
+    out = torch.zeros(c.n, c.Hq, c.D, dtype=torch.float64)
+    tol = torch.zeros_like(out)
+    for s in range(len(c.kv)):
+        r = slice(int(c.cu[s]), int(c.cu[s + 1]))
+        for h in range(c.Hq):
+            t, x, err = ref.logits(c, s, h, window, sinks, scale)
+            if not len(t) or not c.rows[s]:
+                continue
+            v = c.tokens(c.v, s, h // (c.Hq // c.Hkv))[1]
+            l = torch.logsumexp(x, 1, keepdim=True)
+            p = torch.where(l > -math.inf, (x - l).exp(), 0.0)
+            o, a = p @ v, p @ v.abs()
+            out[r, h] = o
+            # one rounding of the result, half a step (2^-8); a weight within 2^-16 of
+            # itself (two bf16 parts), moved by twice the logits' error; 2^-15 for fp32 sums
+            tol[r, h] = 2.0 ** -8 * o.abs() + (2.0 ** -16 + 2 * err + 2.0 ** -15) * a * (1 + 2.0 ** -7)
+    return out, tol
+
+
+PRECISION = [([40, 23, 9, 65], [19, 23, 5, 40]), ([31, 12], [1, 1]), ([150, 33, 260], [4, 1, 130])]
+
+
+@gpu
+@pytest.mark.parametrize("extra_pages", [1, 1100])  # the second: the form for long caches, whatever the rows
+@pytest.mark.parametrize("heads", [(8, 2, 64), (16, 16, 64), (32, 8, 128), (8, 1, 128)])
+@pytest.mark.parametrize("kv,rows", PRECISION)
+def test_attend_weights_keep_more_than_one_bf16(kv, rows, heads, extra_pages):
+    c = Cache(kv, rows, *heads, seed=61, extra_pages=extra_pages)
+    out, _ = ref.run_attend(c)
+    want, tol = _attend(c)
+    ref.check(out, want, tol, "out")
+    out, _ = ref.run_attend(c, 20, 3, 0.4)
+    want, tol = _attend(c, 20, 3, 0.4)
+    ref.check(out, want, tol, "out")
+
+
+def test_one_bf16_of_the_weights_is_outside_that_bound():
+    # the plain computation with weights of one bf16, everything else in 64 bits
+    for kv, rows in PRECISION:
+        c = Cache(kv, rows, 8, 2, 64, seed=61, device="cpu")
+        want, tol = _attend(c)
+        got = torch.zeros_like(want)
+        for s in range(len(kv)):
+            r = slice(int(c.cu[s]), int(c.cu[s + 1]))
+            for h in range(c.Hq):
+                _, x, _ = ref.logits(c, s, h, 0, 0, 1 / 8.0)
+                p = (x - x.amax(1, keepdim=True)).exp()
+                got[r, h] = p.bfloat16().double() @ c.tokens(c.v, s, h // 4)[1] / p.sum(1, keepdim=True)
+        assert bool(((got.bfloat16().double() - want).abs() > tol).any()), (kv, rows)
