@@ -448,7 +448,8 @@ pa_status pa_window_workspace_size(const pa_sessions *b, int32_t window, int32_t
  *   q                 device bf16 [num_rows][Hq][D]
  *   out               device bf16 [num_rows][Hq][D]
  *   lse               device fp32 [num_rows][Hq], natural log; may be NULL
- * A row that sees nothing gets zeros and lse = -inf.  PA_ERR_NOMEM when
+ * A row that sees nothing gets zeros and lse = -inf, one whose logits are NaN (a NaN
+ * in its q) NaN in out and lse.  PA_ERR_NOMEM when
  * workspace_bytes is below pa_window_workspace_size.
  */
 pa_status pa_window_attend(const pa_sessions *b, int32_t window, int32_t sinks, float softmax_scale, const void *q,

@@ -788,7 +788,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n_mine = pair ? n : (n - grp + 1) >> 1;  // blocks of this group
       if (n_mine > 0 && !(ok = wwait(mi.o_full[grp], po++, 15))) break;
       tc_fence_after();
-      float w0 = l > 0.f ? 1.f / l : 0.f, w1 = 0.f, lse2 = l > 0.f ? m + lg2(l) : -INFINITY;
+      // (a sum of 0: the row saw nothing; one that is NaN makes its out and lse NaN)
+      float w0 = l == 0.f ? 0.f : 1.f / l, w1 = 0.f, lse2 = l == 0.f ? -INFINITY : m + lg2(l);
       int d0 = 0, dn = D;  // dims this thread writes
       uint32_t src0 = t_o, src1 = t_o;
       bool two = false;
@@ -804,9 +805,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(mi.joined));  // read by both before the next item's are written
         if (!(ok = wwait(mi.joined, pj++, 17))) break;
         const float mm = fmaxf(m, ml.x);
-        const float f0 = l > 0.f ? ex2(m - mm) : 0.f, f1 = ml.y > 0.f ? ex2(ml.x - mm) : 0.f;
-        const float lt2 = l * f0 + ml.y * f1, inv = lt2 > 0.f ? 1.f / lt2 : 0.f;
-        lse2 = lt2 > 0.f ? mm + lg2(lt2) : -INFINITY;
+        const float f0 = l == 0.f ? 0.f : ex2(m - mm), f1 = ml.y == 0.f ? 0.f : ex2(ml.x - mm);
+        const float lt2 = l * f0 + ml.y * f1, inv = lt2 == 0.f ? 0.f : 1.f / lt2;
+        lse2 = lt2 == 0.f ? -INFINITY : mm + lg2(lt2);
         w0 = f0 * inv;
         w1 = f1 * inv;
         d0 = grp * (D / 2);
@@ -907,7 +908,7 @@ __global__ void __launch_bounds__(256) window_join_kernel(const AttendArgs a) {
 #pragma unroll 4
     for (int c = d.first + rank; c <= d.last; c += team) {
       const size_t at = slot_of(c);
-      const float f = mx == -INFINITY ? 0.f : ex2(a.part_lse[at] - mx);
+      const float pl = a.part_lse[at], f = pl == -INFINITY ? 0.f : ex2(pl - mx);
       sum += f;
 #pragma unroll
       for (int i = 0; i < W; ++i) acc[i] += f * a.part_o[at * D + lane * W + i];
@@ -927,12 +928,12 @@ __global__ void __launch_bounds__(256) window_join_kernel(const AttendArgs a) {
       __syncthreads();
       if (warp) continue;
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     const size_t ro = (size_t)(d.row0 + (prow >> a.lg)) * a.b.Hq + (d.g << a.lg) + (prow & ((1 << a.lg) - 1));
     uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + ro * D) + lane * (W / 2);
 #pragma unroll
     for (int i = 0; i < W; i += 2) dst[i / 2] = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
-    if (a.lse && lane == 0) a.lse[ro] = sum > 0.f ? (mx + lg2(sum)) * kLn2 : -INFINITY;
+    if (a.lse && lane == 0) a.lse[ro] = sum == 0.f ? -INFINITY : (mx + lg2(sum)) * kLn2;
   }
 }
 
@@ -1052,10 +1053,10 @@ __global__ void __launch_bounds__(kShortThreads, 2) window_short_kernel(const At
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float y0 = see0 ? x[i] * a.scale_log2 : -INFINITY, y1 = see1 ? x[2 + i] * a.scale_log2 : -INFINITY;
-      float mx = fmaxf(y0, y1);
+      float mx = max_nan(y0, y1);  // (a maximum that dropped NaN would leave such a row without keys)
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      mx = fmaxf(mx, m[i]);
+      for (int o = 4; o < 32; o <<= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      mx = max_nan(mx, m[i]);
       const float c = m[i] == mx ? 1.f : ex2(m[i] - mx);  // no key yet: 0, of nothing
       const float w0 = y0 == -INFINITY ? 0.f : ex2(y0 - mx), w1 = y1 == -INFINITY ? 0.f : ex2(y1 - mx);
       m[i] = mx;
@@ -1113,13 +1114,13 @@ __global__ void __launch_bounds__(kShortThreads, 2) window_short_kernel(const At
       o.y += f * y.y;
     };
 #pragma unroll
-    for (int w = 0; w < kShortWarps; ++w) mx = fmaxf(mx, top[w][h]);
+    for (int w = 0; w < kShortWarps; ++w) mx = max_nan(mx, top[w][h]);
 #pragma unroll
     for (int w = 0; w < kShortWarps; ++w) add(top[w][h], sums[w][h], *reinterpret_cast<const float2*>(&part[w][h][d]));
     if (C == 1) {
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
       *reinterpret_cast<uint32_t*>(a.out + row + i) = pack_bf16x2(o.x * inv, o.y * inv);
-      if (a.lse && d == 0) a.lse[(size_t)r * a.b.Hq + g * G + h] = sum > 0.f ? (mx + lg2(sum)) * kLn2 : -INFINITY;
+      if (a.lse && d == 0) a.lse[(size_t)r * a.b.Hq + g * G + h] = sum == 0.f ? -INFINITY : (mx + lg2(sum)) * kLn2;
     } else {
       *reinterpret_cast<float2*>(&joined[h][d]) = o;
       if (d == 0) joined_top[h] = mx, joined_sum[h] = sum;
@@ -1135,7 +1136,7 @@ __global__ void __launch_bounds__(kShortThreads, 2) window_short_kernel(const At
 #pragma unroll
     for (int c = 0; c < kShortCluster; ++c) {
       t[c] = c < C ? cluster_read(&joined_top[h], c) : -INFINITY;
-      mx = fmaxf(mx, t[c]);
+      mx = max_nan(mx, t[c]);
     }
 #pragma unroll
     for (int c = 0; c < kShortCluster; ++c) {
@@ -1145,9 +1146,9 @@ __global__ void __launch_bounds__(kShortThreads, 2) window_short_kernel(const At
       o.x += f * cluster_read(&joined[h][d], c);
       o.y += f * cluster_read(&joined[h][d + 1], c);
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
     *reinterpret_cast<uint32_t*>(a.out + row + i) = pack_bf16x2(o.x * inv, o.y * inv);
-    if (a.lse && d == 0) a.lse[(size_t)r * a.b.Hq + g * G + h] = sum > 0.f ? (mx + lg2(sum)) * kLn2 : -INFINITY;
+    if (a.lse && d == 0) a.lse[(size_t)r * a.b.Hq + g * G + h] = sum == 0.f ? -INFINITY : (mx + lg2(sum)) * kLn2;
   }
   __syncwarp();
   cluster_sync();  // no CTA leaves while another reads its results

@@ -67,3 +67,49 @@ def test_one_bf16_of_the_weights_is_outside_that_bound():
                 p = (x - x.amax(1, keepdim=True)).exp()
                 got[r, h] = p.bfloat16().double() @ c.tokens(c.v, s, h // 4)[1] / p.sum(1, keepdim=True)
         assert bool(((got.bfloat16().double() - want).abs() > tol).any()), (kv, rows)
+
+
+# ------------------------------------------------------------------------------------------------ queries that are not numbers
+
+# the form for few rows with one CTA and with a cluster for a row, whole items of one
+# and of two tiles, items cut into parts
+NAN_QUERIES = {
+    "one CTA a row": ([100 + i for i in range(80)], [1] * 80, 1),
+    "a cluster a row": ([1000, 40], [1, 1], 1),
+    "mostly empty cluster": ([20], [1], 60),
+    "one tile": ([60, 33], [5, 9], 1),
+    "two tiles": ([100, 20], [64, 3], 1),
+    "cut": ([9000, 700], [5, 60], 1),
+    "cut into many parts": ([20000], [3], 1),
+}
+
+
+@gpu
+@pytest.mark.parametrize("heads", [(8, 2, 64), (8, 2, 128), (2, 2, 64)])
+@pytest.mark.parametrize("name", list(NAN_QUERIES))
+def test_attend_a_nan_query_gives_nan_and_stays_alone(name, heads):
+    kv, rows, extra = NAN_QUERIES[name]
+    c = Cache(kv, rows, *heads, seed=71, extra_pages=extra)
+    clean, clean_lse = ref.run_attend(c)
+    assert not bool(clean.isnan().any()) and not bool(clean_lse.isnan().any())
+    bad = [(0, 1), (c.n - 1, heads[0] - 1)]
+    for r, h in bad:
+        c.q[r, h, 3] = math.nan
+    out, lse = ref.run_attend(c)
+    hit = torch.zeros(lse.shape, dtype=torch.bool)
+    for r, h in bad:
+        hit[r, h] = True
+    assert torch.equal(lse.isnan().cpu(), hit), name
+    assert torch.equal(out.isnan().cpu(), hit[..., None].expand(out.shape)), name
+    ok = ~hit.cuda()
+    assert torch.equal(out[ok], clean[ok]) and torch.equal(lse[ok], clean_lse[ok])
+
+
+@gpu
+@pytest.mark.parametrize("rows", [1, 40])
+def test_attend_a_row_without_keys_is_empty_even_with_a_nan_query(rows):
+    c = Cache([rows + 5, 0], [rows, rows], 4, 2, 64, seed=72)
+    c.q[rows:] = math.nan  # session 1 has no cached tokens
+    out, lse = ref.run_attend(c)
+    assert bool((out[rows:] == 0).all()) and bool((lse[rows:] == -math.inf).all())
+    assert not bool(out[:rows].isnan().any())
