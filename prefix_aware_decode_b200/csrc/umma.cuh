@@ -10,10 +10,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-// The larger one; NaN if either is.
+// The larger, the smaller one; NaN if either is.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
 }
 __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
@@ -87,12 +92,13 @@ __device__ __forceinline__ void tmem_scale8(uint32_t taddr, float f) {
                : "memory");
 }
 
-// 2^x of two finite x <= 127 on the FMA pipe: x = n + f, f in [-1/2, 1/2]; 2^f by
-// the degree-5 polynomial of least relative error (Remez exchange, 7.5e-8), n
-// added to the exponent.  x below -126 counts as -126.
+// 2^x of two x on the FMA pipe: x = n + f, f in [-1/2, 1/2]; 2^f by the degree-5
+// polynomial of least relative error (Remez exchange, 7.5e-8) times 2^n, made of its
+// bits.  As ex2 at the ends: 0 below -126.5 (-inf among it), inf from 127.5 on, NaN of NaN
+// (which the clamps keep and the product then carries).
 __device__ __forceinline__ float2 exp2_fma(float2 x) {
-  x.x = fmaxf(x.x, -126.f);
-  x.y = fmaxf(x.y, -126.f);
+  x.x = min_nan(max_nan(x.x, -127.f), 128.f);
+  x.y = min_nan(max_nan(x.y, -127.f), 128.f);
   // adding 1.5 * 2^23 rounds to an integer, which its low bits then hold
   const float2 t = fadd2(x, make_float2(12582912.f, 12582912.f));
   const float2 n = fadd2(t, make_float2(-12582912.f, -12582912.f));
@@ -103,9 +109,8 @@ __device__ __forceinline__ float2 exp2_fma(float2 x) {
   p = ffma2(p, f, make_float2(0.24022120237350464f, 0.24022120237350464f));
   p = ffma2(p, f, make_float2(0.6931469440460205f, 0.6931469440460205f));
   p = ffma2(p, f, make_float2(1.0000001192092896f, 1.0000001192092896f));
-  p.x = __uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23));
-  p.y = __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23));
-  return p;
+  return fmul2(p, make_float2(__uint_as_float(0x3f800000u + (__float_as_uint(t.x) << 23)),
+                              __uint_as_float(0x3f800000u + (__float_as_uint(t.y) << 23))));
 }
 
 }  // namespace pa

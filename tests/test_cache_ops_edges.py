@@ -113,3 +113,82 @@ def test_attend_a_row_without_keys_is_empty_even_with_a_nan_query(rows):
     out, lse = ref.run_attend(c)
     assert bool((out[rows:] == 0).all()) and bool((lse[rows:] == -math.inf).all())
     assert not bool(out[:rows].isnan().any())
+
+
+# ------------------------------------------------------------------------------------------------ weights of single columns
+
+
+def _columns(D=64):
+    """16 rows of 8 heads over 144 tokens: every row sees the first 128 tokens, so the
+    128 (row, head) columns and 128 keys make one full tile.  A column's lse of -inf
+    takes it out (it weighs nothing), which leaves one weight per key."""
+    c = Cache([144], [16], 8, 1, D, seed=81)
+    c.q.zero_()
+    c.q[..., 0] = c.q[..., 1] = 1.0
+    c.k.zero_()
+    return c
+
+
+def _put(c, x):
+    """The logits of the first 128 tokens, with a scale of ln 2: x octaves, in two bf16 parts."""
+    t = torch.arange(128)
+    hi = x.bfloat16()
+    lo = (x - hi.double()).bfloat16()
+    c.k[c.table[0, t // 16].long(), 0, t % 16, 0] = hi
+    c.k[c.table[0, t // 16].long(), 0, t % 16, 1] = lo
+    return hi.double() + lo.double()
+
+
+def _weigh_column(c, col, lse=0.0):
+    l = torch.full((16, 8), -math.inf, device="cuda")
+    l[col // 8, col % 8] = lse
+    scores = torch.zeros(1, 1, 144, device="cuda")
+    q, k, table, lens, cu = c.dev("q", "k", "table", "lens", "cu")
+    ref.pad.weigh_tokens(q, k, l, table, lens, cu, scores, softmax_scale=math.log(2.0))
+    return scores[0, 0, :128].double().cpu()
+
+
+@gpu
+def test_weigh_every_column_computes_the_same_weight():
+    c = _columns()
+    x = _put(c, torch.linspace(-1.0, 1.0, 128, dtype=torch.float64))
+    scale = torch.tensor(math.log(2.0)).float() * torch.tensor(1.4426950408889634).float()
+    want = 2.0 ** (x * scale.double())
+    for col in range(128):
+        got = _weigh_column(c, col)
+        # the argument to half a step of numbers up to 1 (2^-24, times ln 2 in the weight),
+        # the exponential and its last rounding: 2^-22 in all
+        assert bool(((got - want).abs() <= 2.0 ** -22 * want).all()), (col, float(((got - want) / want).abs().max()))
+
+
+@gpu
+def test_weigh_every_column_over_the_whole_range_of_exponents():
+    c = _columns()
+    x = _put(c, torch.linspace(-160.0, 100.0, 128, dtype=torch.float64))
+    want = 2.0 ** x
+    for col in range(128):
+        got = _weigh_column(c, col)
+        # the scale is ln 2 log2 e in fp32: off by 2^-24 each way, on an argument of up to 160
+        tol = want * 2.0 ** -15 + torch.where(x < -125.0, 2.0 ** -126, 0.0)  # below: flushed or not
+        assert bool(((got - want).abs() <= tol).all()), col
+    x = _put(c, torch.linspace(129.0, 400.0, 128, dtype=torch.float64))
+    for col in range(128):
+        assert bool((_weigh_column(c, col) == math.inf).all()), col
+
+
+@gpu
+def test_weigh_a_row_of_lse_minus_infinity_weighs_nothing():
+    c = _columns()
+    _put(c, torch.linspace(-3.0, 3.0, 128, dtype=torch.float64))
+    assert bool((_weigh_column(c, 0, -math.inf) == 0).all())
+
+
+@gpu
+def test_weigh_a_nan_query_or_lse_reaches_every_score_it_draws_on():
+    c = _columns()
+    _put(c, torch.linspace(-3.0, 3.0, 128, dtype=torch.float64))
+    for col in range(128):
+        assert bool(_weigh_column(c, col, math.nan).isnan().all()), col
+        c.q[col // 8, col % 8, 5] = math.nan
+        assert bool(_weigh_column(c, col).isnan().all()), col
+        c.q[col // 8, col % 8, 5] = 0.0
