@@ -192,3 +192,11 @@ def test_weigh_a_nan_query_or_lse_reaches_every_score_it_draws_on():
         c.q[col // 8, col % 8, 5] = math.nan
         assert bool(_weigh_column(c, col).isnan().all()), col
         c.q[col // 8, col % 8, 5] = 0.0
+
+
+@gpu
+def test_weigh_a_logit_equal_to_its_lse_weighs_exactly_one():
+    c = _columns()
+    _put(c, torch.zeros(128, dtype=torch.float64))
+    for col in range(128):
+        assert bool((_weigh_column(c, col) == 1.0).all()), col
