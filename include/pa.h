@@ -380,7 +380,8 @@ pa_status pa_attend_noalloc(const pa_plan *plan, const void *q, const void *k_po
  *                    as they were.  pa_evict_tokens does not read it (NULL).
  * The i-th of the n rows of a session is its cached token kv_len - n + i (its
  * position).  A block-table entry outside [0, num_pages_in_pool) is a hole: its
- * tokens are neither written, seen nor copied.  The K and V of tokens that some
+ * tokens are neither written, seen nor copied (pa_evict_tokens says what it does
+ * when it keeps one).  The K and V of tokens that some
  * row sees are finite; other tokens and slots may hold anything, NaN included.
  * The device arrays are read when the kernels run.  Arguments are checked
  * before anything is enqueued: PA_ERR_INVALID for a null or misaligned pointer
@@ -485,7 +486,11 @@ pa_status pa_weigh_status(void *stream, pa_status *out);
  * them when there are no more); equal scores keep the lower index, NaN ranks
  * above every number.  The kept tokens go, in order, to the session's row of
  * the destination table, each kv head its own tokens: the result is an
- * ordinary paged cache of min(kv_len, budget) tokens.
+ * ordinary paged cache of min(kv_len, budget) tokens.  Tokens in holes are ranked
+ * by their scores like others, and a kept one's slot, which is no hole any more,
+ * gets K and V of zeros (never what its page held before): it will be seen.  A
+ * caller who drops pages scores their tokens -inf, which keeps them only where
+ * sinks, recent or a budget that is not reached hold them.
  *   scores            device fp32 [S][Hkv][max_tokens] (as pa_weigh_tokens);
  *                     kv_len is taken as at most max_tokens
  *   d_dst_table       device int32 [S][dst_max_pages], dst_max_pages * P >=

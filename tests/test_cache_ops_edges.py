@@ -200,3 +200,39 @@ def test_weigh_a_logit_equal_to_its_lse_weighs_exactly_one():
     _put(c, torch.zeros(128, dtype=torch.float64))
     for col in range(128):
         assert bool((_weigh_column(c, col) == 1.0).all()), col
+
+
+# ------------------------------------------------------------------------------------------------ eviction and holes
+
+
+@gpu
+@pytest.mark.parametrize("kv,budget,sinks,recent", [(100, 40, 4, 8), (30, 64, 0, 0), (1500, 700, 3, 17), (48, 48, 0, 0)])
+def test_evict_brings_no_stale_memory_out_of_a_hole(kv, budget, sinks, recent):
+    D, Hkv = 64, 2
+    c = Cache([kv], [1], 4, Hkv, D, seed=91)
+    holes = [0, 1, (kv - 1) // 16]
+    n_dst = -(-budget // 16)
+    base = c.num_pages
+    spare = torch.full((n_dst, Hkv, 16, D), math.nan).bfloat16()  # what the pages held before
+    k0, v0 = torch.cat([c.k, spare]), torch.cat([c.v, spare])
+    for i, j in enumerate(holes):
+        c.table[0, j] = (-1, base + n_dst, 2 ** 31 - 1)[i]
+    scores = torch.rand(1, Hkv, c.width * 16, generator=c.gen)
+    kept = ref.evict(scores, [kv], budget, sinks, recent)[0]
+    k, v = k0.cuda(), v0.cuda()
+    table, lens, cu, q = c.dev("table", "lens", "cu", "q")
+    dst = (base + torch.arange(n_dst).int()).view(1, -1).cuda()
+    new, got, _ = ref.pad.evict_tokens(scores.cuda(), k, v, table, lens, dst, budget, sinks=sinks, recent=recent)
+    m = min(kv, budget)
+    assert new.tolist() == [m]
+    for h in range(Hkv):
+        assert got[0, h, :m].tolist() == kept[h]
+        t = torch.tensor(kept[h])
+        gone = torch.tensor([j in holes for j in (t // 16).tolist()])
+        for pool, old in ((k, k0), (v, v0)):
+            row = pool[base:, h].reshape(-1, D)[:m].cpu()
+            assert bool((row[gone] == 0).all()), "a slot kept what its page held before"
+            src = old[c.table[0, t[~gone] // 16].long(), h, t[~gone] % 16]
+            assert torch.equal(row[~gone], src)
+    out, lse = ref.pad.window_attend(q, k, v, dst, new, cu)
+    assert not bool(out.isnan().any()) and not bool(lse.isnan().any())
