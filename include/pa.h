@@ -458,7 +458,7 @@ pa_status pa_window_attend(const pa_sessions *b, int32_t window, int32_t sinks, 
                            void *out, float *lse, void *stream);
 
 /* The device status word that the last pa_window_attend on this workspace left:
- * PA_OK, or PA_ERR_TIMEOUT when a device-side bounded wait gave up (its results
+ * PA_OK (also after a call of 0 rows), or PA_ERR_TIMEOUT when a device-side bounded wait gave up (its results
  * are then not to be used).  Synchronises `stream`. */
 pa_status pa_window_status(const void *d_workspace, void *stream, pa_status *out);
 

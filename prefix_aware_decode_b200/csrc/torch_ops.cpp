@@ -169,7 +169,9 @@ Tensor window_workspace(const Tensor& q, const Tensor& k_pool, const Tensor& tab
   q_rows(q, k_pool, index);
   const pa_sessions b = sessions(k_pool, table, kv_lens, &cu_rows, q.size(0), q.size(1), index);
   const c10::cuda::CUDAGuard on(index);
-  return make({(int64_t)workspace_bytes(b, window, sinks)}, at::kByte, index);
+  Tensor ws = make({(int64_t)workspace_bytes(b, window, sinks)}, at::kByte, index);
+  ws.narrow(0, 0, 256).zero_();  // the status of no call yet
+  return ws;
 }
 
 std::tuple<Tensor, Tensor> window_attend(const Tensor& q, const Tensor& k_pool, const Tensor& v_pool,

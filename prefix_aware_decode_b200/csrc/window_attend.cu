@@ -1277,7 +1277,12 @@ extern "C" pa_status pa_window_attend(const pa_sessions* b, int32_t window, int3
   if (window < 0 || sinks < 0 || !(softmax_scale >= 0.f) || softmax_scale > 3.4e38f) return PA_ERR_INVALID;
   pa::Launch l;
   if (!pa::plan_launch(*b, pa_window(window, sinks), &l)) return PA_ERR_UNSUPPORTED;
-  if (b->num_rows == 0) return PA_OK;
+  if (b->num_rows == 0) {  // nothing but the status of a workspace that is given
+    if (!d_workspace) return PA_OK;
+    if (reinterpret_cast<uintptr_t>(d_workspace) & 255) return PA_ERR_INVALID;
+    if (workspace_bytes < l.bytes) return PA_ERR_NOMEM;
+    return cudaMemsetAsync(d_workspace, 0, 4, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  }
   if (!q || !k_pool || !v_pool || !out || !d_workspace) return PA_ERR_INVALID;
   if (!pa_aligned16(q) || !pa_aligned16(k_pool) || !pa_aligned16(v_pool) || !pa_aligned16(out) ||
       (reinterpret_cast<uintptr_t>(d_workspace) & 255))

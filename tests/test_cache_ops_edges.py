@@ -236,3 +236,19 @@ def test_evict_brings_no_stale_memory_out_of_a_hole(kv, budget, sinks, recent):
             assert torch.equal(row[~gone], src)
     out, lse = ref.pad.window_attend(q, k, v, dst, new, cu)
     assert not bool(out.isnan().any()) and not bool(lse.isnan().any())
+
+
+# ------------------------------------------------------------------------------------------------ status
+
+
+@gpu
+def test_window_status_of_calls_that_do_nothing():
+    c = Cache([20, 5], [0, 0], 8, 2, 64, seed=95)
+    q, k, v, table, lens, cu = c.dev("q", "k", "v", "table", "lens", "cu")
+    ws = ref.pad.window_workspace(q, k, table, lens, cu)
+    ws.fill_(255)
+    out, lse = ref.pad.window_attend(q, k, v, table, lens, cu, workspace=ws)
+    assert out.shape == (0, 8, 64) and lse.shape == (0, 8)
+    assert ref.pad.window_status(ws) == ref.pad.PA_OK
+    fresh = ref.pad.window_workspace(q, k, table, lens, cu)
+    assert ref.pad.window_status(fresh) == ref.pad.PA_OK
