@@ -458,8 +458,10 @@ pa_status pa_window_attend(const pa_sessions *b, int32_t window, int32_t sinks, 
                            void *out, float *lse, void *stream);
 
 /* The device status word that the last pa_window_attend on this workspace left:
- * PA_OK (also after a call of 0 rows), or PA_ERR_TIMEOUT when a device-side bounded wait gave up (its results
- * are then not to be used).  Synchronises `stream`. */
+ * PA_OK (also after a call of 0 rows), or PA_ERR_TIMEOUT when a device-side
+ * bounded wait gave up (its results are then not to be used).  d_workspace NULL:
+ * the first failure of any pa_window_attend on the current device since this form
+ * last returned one, for callers who keep no workspace.  Synchronises `stream`. */
 pa_status pa_window_status(const void *d_workspace, void *stream, pa_status *out);
 
 /*

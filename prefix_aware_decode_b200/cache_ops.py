@@ -37,6 +37,11 @@ def _on(stream, device):
     return torch.cuda.stream(stream)
 
 
+def _index(device) -> int:
+    index = None if device is None else torch.device(device).index
+    return torch.cuda.current_device() if index is None else index
+
+
 def rope_append(q, k, v, positions, inv_freq, k_pool, v_pool, block_table, kv_lens, cu_rows, *,
                 axes: Optional[Sequence[int]] = None, interleaved: bool = False, q_out=None, stream=None):
     """Rotates the rows' q and k and writes k and v into their cache slots
@@ -65,13 +70,16 @@ def window_workspace(q, k_pool, block_table, kv_lens, cu_rows, *, window: int = 
     return _ops.window_workspace(q, k_pool, block_table, kv_lens, cu_rows, window, sinks)
 
 
-def window_status(workspace, stream=None) -> int:
+def window_status(workspace=None, stream=None, device=None) -> int:
     """The device status word of the last window_attend on this workspace
-    (pa_window_status; PA_OK unless a bounded wait gave up).  Synchronises the stream."""
+    (pa_window_status; PA_OK unless a bounded wait gave up: the results are then not
+    to be used).  Without a workspace: the first failure of any window_attend on the
+    device since this call last returned one.  Synchronises the stream."""
+    index = _index(device) if workspace is None else -1
     if stream is not None:
-        with _on(stream, workspace.device):
-            return _ops.window_status(workspace)
-    return _ops.window_status(workspace)
+        with _on(stream, torch.device("cuda", index) if workspace is None else workspace.device):
+            return _ops.window_status(workspace, index)
+    return _ops.window_status(workspace, index)
 
 
 def window_attend(q, k_pool, v_pool, block_table, kv_lens, cu_rows, *, window: int = 0, sinks: int = 0,
@@ -83,7 +91,8 @@ def window_attend(q, k_pool, v_pool, block_table, kv_lens, cu_rows, *, window: i
     q bf16 [rows][Hq][D]; pools bf16 [num_pages][Hkv][P][D].  Returns (out bf16
     [rows][Hq][D], lse fp32 [rows][Hq]); rows that see nothing get 0 and -inf, rows
     of no session are not written (undefined in tensors that the call allocates).
-    `workspace` (window_workspace) is allocated by the call when not given.
+    `workspace` (window_workspace) is allocated by the call when not given;
+    window_status() then tells whether a call gave up.
     """
     if stream is not None:
         with _on(stream, k_pool.device):
@@ -107,8 +116,7 @@ def weigh_tokens(q, k_pool, lse, block_table, kv_lens, cu_rows, scores, *, windo
 def weigh_status(device=None, stream=None) -> int:
     """The first failure of a bounded wait of weigh_tokens on the device since this
     call last returned one (pa_weigh_status; PA_OK: none).  Synchronises the stream."""
-    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    index = torch.cuda.current_device() if device.index is None else device.index
+    index = _index(device)
     if stream is not None:
         with _on(stream, torch.device("cuda", index)):
             return _ops.weigh_status(index)

@@ -149,6 +149,20 @@ inline pa_device pa_current_device() {
   return d;
 }
 
+// Reads the first-failure word of the current device (a __device__ array of four)
+// and clears it when it tells of one; synchronises the stream.
+template <typename W>
+pa_status pa_take_status(const W& words, cudaStream_t cs, pa_status* out) {
+  void* word = nullptr;
+  int32_t v = 0;
+  if (cudaGetSymbolAddress(&word, words) != cudaSuccess ||
+      cudaMemcpyAsync(&v, word, 4, cudaMemcpyDeviceToHost, cs) != cudaSuccess || cudaStreamSynchronize(cs) != cudaSuccess)
+    return PA_ERR_CUDA;
+  if (v != 0 && cudaMemsetAsync(word, 0, sizeof(W), cs) != cudaSuccess) return PA_ERR_CUDA;
+  *out = static_cast<pa_status>(v);
+  return PA_OK;
+}
+
 // Launch of a kernel that begins with griddep_wait (before it touches memory): it
 // may be brought up while the kernel before it on the stream still runs.
 template <typename... P, typename... A>

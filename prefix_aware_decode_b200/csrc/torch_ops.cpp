@@ -196,10 +196,11 @@ std::tuple<Tensor, Tensor> window_attend(const Tensor& q, const Tensor& k_pool, 
   return {o, l};
 }
 
-int window_status(const Tensor& workspace) {
-  if (!workspace.is_cuda()) bad("workspace must be a CUDA tensor");
-  const auto index = workspace.get_device();
-  const void* wp = ptr(workspace, "workspace", at::kByte, index, 256);
+// Of a workspace, or of every call on a device.
+int window_status(const std::optional<Tensor>& workspace, int64_t device) {
+  if (workspace && !workspace->is_cuda()) bad("workspace must be a CUDA tensor");
+  const auto index = workspace ? workspace->get_device() : static_cast<c10::DeviceIndex>(device);
+  const void* wp = workspace ? ptr(*workspace, "workspace", at::kByte, index, 256) : nullptr;
   const c10::cuda::CUDAGuard on(index);
   pa_status st = PA_OK;
   void* stream = current(index);

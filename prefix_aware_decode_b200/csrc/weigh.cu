@@ -657,14 +657,5 @@ extern "C" pa_status pa_weigh_tokens(const pa_sessions* b, int32_t window, int32
 
 extern "C" pa_status pa_weigh_status(void* stream, pa_status* out) {
   if (!out) return PA_ERR_INVALID;
-  cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  void* word = nullptr;
-  int32_t v = 0;
-  if (cudaGetSymbolAddress(&word, pa::g_weigh_status) != cudaSuccess ||
-      cudaMemcpyAsync(&v, word, 4, cudaMemcpyDeviceToHost, cs) != cudaSuccess ||
-      cudaStreamSynchronize(cs) != cudaSuccess)
-    return PA_ERR_CUDA;
-  if (v != 0 && cudaMemsetAsync(word, 0, 16, cs) != cudaSuccess) return PA_ERR_CUDA;
-  *out = static_cast<pa_status>(v);
-  return PA_OK;
+  return pa_take_status(pa::g_weigh_status, static_cast<cudaStream_t>(stream), out);
 }

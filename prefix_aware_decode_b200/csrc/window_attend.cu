@@ -75,6 +75,9 @@ constexpr int kTwinRows = 64;        // most rows of an item that has each in tw
 constexpr float kRaise = 8.f;        // log2 growth of a maximum that raises it
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
+// First failure of a device-side wait since pa_window_status(NULL, ...) last read it.
+__device__ int32_t g_window_status[4];
+
 struct Desc {  // a partial item at the head of a CTA's span
   int first, last;  // spans that share the item
   int slot0;        // partial slot of the first
@@ -213,6 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
       a.desc[blockIdx.x].first = -1;
       record_status(a.status, PA_ERR_DEVICE, blockIdx.x, 0);
+      record_status(g_window_status, PA_ERR_DEVICE, blockIdx.x, 0);
     }
     return;
   }
@@ -341,6 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           *fail = 1;
           record_status(a.status, PA_ERR_TIMEOUT, blockIdx.x, code);
+          record_status(g_window_status, PA_ERR_TIMEOUT, blockIdx.x, code);
         }
         return false;
       }
@@ -1224,9 +1229,10 @@ extern "C" pa_status pa_window_workspace_size(const pa_sessions* b, int32_t wind
 }
 
 extern "C" pa_status pa_window_status(const void* d_workspace, void* stream, pa_status* out) {
-  if (!d_workspace || !out) return PA_ERR_INVALID;
-  int32_t word = 0;
+  if (!out) return PA_ERR_INVALID;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (!d_workspace) return pa_take_status(pa::g_window_status, cs, out);
+  int32_t word = 0;
   if (cudaMemcpyAsync(&word, d_workspace, 4, cudaMemcpyDeviceToHost, cs) != cudaSuccess) return PA_ERR_CUDA;
   if (cudaStreamSynchronize(cs) != cudaSuccess) return PA_ERR_CUDA;
   *out = static_cast<pa_status>(word);

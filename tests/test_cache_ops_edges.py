@@ -252,3 +252,11 @@ def test_window_status_of_calls_that_do_nothing():
     assert ref.pad.window_status(ws) == ref.pad.PA_OK
     fresh = ref.pad.window_workspace(q, k, table, lens, cu)
     assert ref.pad.window_status(fresh) == ref.pad.PA_OK
+
+
+@gpu
+def test_window_status_needs_no_workspace():
+    c = Cache([2000], [40], 8, 2, 64, seed=96)
+    ref.run_attend(c)
+    s = torch.cuda.Stream()
+    assert ref.pad.window_status() == ref.pad.window_status(device="cuda:0", stream=s) == ref.pad.PA_OK
