@@ -78,7 +78,7 @@ class PaRope(ctypes.Structure):
 EXPORTS = ["pa_plan_create", "pa_plan_advance", "pa_plan_create_append", "pa_plan_workspace_size", "pa_plan_upload", "pa_forward", "pa_merge", "pa_merge_f32", "pa_merge_rows", "pa_attend",
            "pa_get_device_status", "pa_plan_get_stats", "pa_plan_host_image", "pa_plan_set_profile_events",
            "pa_decode_step", "pa_attend_noalloc", "pa_rope_append", "pa_window_workspace_size", "pa_window_attend",
-           "pa_window_status", "pa_weigh_tokens", "pa_weigh_status", "pa_evict_tokens", "pa_plan_destroy", "pa_status_string"]
+           "pa_window_status", "pa_weigh_tokens", "pa_weigh_status", "pa_evict_tokens", "pa_session_fault", "pa_plan_destroy", "pa_status_string"]
 
 _lib = None
 
@@ -141,6 +141,8 @@ def lib() -> ctypes.CDLL:
     L.pa_weigh_status.restype = st
     L.pa_evict_tokens.argtypes = [sp, vp, i64, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp]
     L.pa_evict_tokens.restype = st
+    L.pa_session_fault.argtypes = [i32]
+    L.pa_session_fault.restype = st
     L.pa_plan_destroy.argtypes = [vp]
     L.pa_plan_destroy.restype = None
     L.pa_status_string.argtypes = [st]

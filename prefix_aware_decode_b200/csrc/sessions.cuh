@@ -149,6 +149,14 @@ inline pa_device pa_current_device() {
   return d;
 }
 
+// The wait that the thread's next call gives up (pa_session_fault), taken once.
+inline thread_local int32_t pa_fault = 0;
+inline int32_t pa_take_fault() {
+  const int32_t wait = pa_fault;
+  pa_fault = 0;
+  return wait;
+}
+
 // Reads the first-failure word of the current device (a __device__ array of four)
 // and clears it when it tells of one; synchronises the stream.
 template <typename W>

@@ -57,6 +57,7 @@ struct WeighArgs {
   int nk, nq;             // ring slots of first (and of second) K blocks, and of Q tiles
   int run;                // 1: contiguous runs of items, 0: every gridDim.x-th item
   int pair;               // key blocks of an item: 2, or 1
+  int give_up;            // the wait (its code) that gives up at once; 0: none
   const float* lse;
   float* scores;
   int64_t max_tokens;
@@ -135,7 +136,9 @@ struct Ring {
   }
 };
 
-template <int D>
+// FAULT: the kernel of a call whose waits of one number give up (pa_session_fault); a
+// comparison in every wait would cost all calls 3-8 %
+template <int D, bool FAULT>
 __global__ void __launch_bounds__(kThreads, 1)
     weigh_kernel(const WeighArgs a, const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk) {
   using S = Shape<D>;
@@ -211,11 +214,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* fail = &mi.fail;
   auto wwait = [&](uint64_t& b, int phase, int code) -> bool {
     const uint32_t ad = bar(b), par = (uint32_t)phase & 1u;
-    if (__all_sync(0xffffffffu, mbar_try_wait(ad, par))) return true;
+    const bool quit = FAULT && code == a.give_up;
+    if (!quit && __all_sync(0xffffffffu, mbar_try_wait(ad, par))) return true;
     const uint64_t t0 = global_timer_ns();
-    while (!__all_sync(0xffffffffu, mbar_try_wait(ad, par))) {
+    while (quit || !__all_sync(0xffffffffu, mbar_try_wait(ad, par))) {
       if (__any_sync(0xffffffffu, *fail != 0)) return false;
-      if (__any_sync(0xffffffffu, global_timer_ns() - t0 > kTimeoutNs)) {
+      if (quit || __any_sync(0xffffffffu, global_timer_ns() - t0 > kTimeoutNs)) {
         if (lane == 0) {
           *fail = 1;
           record_status(g_weigh_status, PA_ERR_TIMEOUT, blockIdx.x, code);
@@ -625,9 +629,10 @@ pa_status launch(WeighArgs& a, const pa_sessions& b, const void* q, const void* 
   a.nk = (Shape<D>::SLOTS - a.nq) / a.pair;
   a.per_group = (b.n_sessions + kGroups - 1) / kGroups;
   constexpr int smem = weigh_smem<D>();
-  static std::atomic<uint64_t> allowed{0};
-  if (!pa_allow_smem(weigh_kernel<D>, smem, dev.index, allowed)) return PA_ERR_CUDA;
-  return pa_launch_early(weigh_kernel<D>, dim3(grid), dim3(kThreads), smem, cs, 1, a, tq, tk) ? PA_OK : PA_ERR_CUDA;
+  auto* kernel = a.give_up ? weigh_kernel<D, true> : weigh_kernel<D, false>;
+  static std::atomic<uint64_t> allowed[2];
+  if (!pa_allow_smem(kernel, smem, dev.index, allowed[a.give_up ? 1 : 0])) return PA_ERR_CUDA;
+  return pa_launch_early(kernel, dim3(grid), dim3(kThreads), smem, cs, 1, a, tq, tk) ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace
@@ -647,6 +652,7 @@ extern "C" pa_status pa_weigh_tokens(const pa_sessions* b, int32_t window, int32
   a.w = pa_window(window, sinks);
   const int G = b->num_q_heads / b->num_kv_heads;
   a.lg = G == 8 ? 3 : G == 4 ? 2 : G == 2 ? 1 : 0;
+  a.give_up = pa_take_fault();
   a.lse = lse;
   a.scores = scores;
   a.max_tokens = max_tokens;

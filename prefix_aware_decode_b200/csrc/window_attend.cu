@@ -90,6 +90,7 @@ struct AttendArgs {
   int lg;              // log2 G
   int slots, min_span, lanes;
   int whole;           // items are not cut: a CTA takes those that start in its span
+  int give_up;         // the wait (its code) that gives up at once; 0: none
   float scale_log2;
   uint16_t* out;
   float* lse;
@@ -204,7 +205,9 @@ struct Sums {
 };
 static_assert(sizeof(Sums) <= 5 * Shape<64>::TILE, "ring");
 
-template <int D>
+// FAULT: the kernel of a call whose waits of one number give up (pa_session_fault); a
+// comparison in every wait would cost all calls 3 %
+template <int D, bool FAULT>
 __global__ void __launch_bounds__(kThreads, 1)
     window_attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap tq,
                          const __grid_constant__ CUtensorMap tq16, const __grid_constant__ CUtensorMap tk,
@@ -337,15 +340,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   // is uniform (a loop that lanes leave one by one took 100 cycles).
   auto wwait = [&](uint64_t& b, int phase, int code) -> bool {
     const uint32_t ad = bar(b), par = (uint32_t)phase & 1u;
-    if (__all_sync(0xffffffffu, mbar_try_wait(ad, par))) return true;
+    const bool quit = FAULT && code == a.give_up;
+    if (!quit && __all_sync(0xffffffffu, mbar_try_wait(ad, par))) return true;
     const uint64_t t0 = global_timer_ns();
-    while (!__all_sync(0xffffffffu, mbar_try_wait(ad, par))) {
+    while (quit || !__all_sync(0xffffffffu, mbar_try_wait(ad, par))) {
       if (__any_sync(0xffffffffu, *fail != 0)) return false;
-      if (__any_sync(0xffffffffu, global_timer_ns() - t0 > kTimeoutNs)) {
+      if (quit || __any_sync(0xffffffffu, global_timer_ns() - t0 > kTimeoutNs)) {
         if (lane == 0) {
           *fail = 1;
           record_status(a.status, PA_ERR_TIMEOUT, blockIdx.x, code);
-          record_status(g_window_status, PA_ERR_TIMEOUT, blockIdx.x, code);
         }
         return false;
       }
@@ -879,7 +882,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (*fail) settle();
+  if (*fail) {
+    if (tid == 0) record_status(g_window_status, PA_ERR_TIMEOUT, blockIdx.x, 0);
+    settle();
+  }
   griddep_launch_dependents();
   if (warp == 8) tmem_free(tmem, 512);
 }
@@ -1239,6 +1245,12 @@ extern "C" pa_status pa_window_status(const void* d_workspace, void* stream, pa_
   return PA_OK;
 }
 
+extern "C" pa_status pa_session_fault(int32_t wait) {
+  if (wait < 0) return PA_ERR_INVALID;
+  pa_fault = wait;
+  return PA_OK;
+}
+
 namespace {
 
 template <int D, int G>
@@ -1264,10 +1276,10 @@ bool launch_short(const pa::AttendArgs& a, int cluster, const void* q, const voi
 template <int D>
 bool launch(const pa::AttendArgs& a, const pa::Launch& l, const CUtensorMap& tq, const CUtensorMap& tq16,
             const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t cs) {
-  auto* k = pa::window_attend_kernel<D>;
+  auto* k = a.give_up ? pa::window_attend_kernel<D, true> : pa::window_attend_kernel<D, false>;
   constexpr int smem = pa::Shape<D>::SMEM;
-  static std::atomic<uint64_t> allowed{0};
-  if (!pa_allow_smem(k, smem, l.device, allowed)) return false;
+  static std::atomic<uint64_t> allowed[2];
+  if (!pa_allow_smem(k, smem, l.device, allowed[a.give_up ? 1 : 0])) return false;
   if (!pa_launch_early(k, dim3(l.grid), dim3(pa::kThreads), smem, cs, 1, a, tq, tq16, tk, tv)) return false;
   if (l.grid == l.lanes || a.whole) return true;  // no item is cut
   return pa_launch_early(pa::window_join_kernel<D>, dim3(l.grid - l.lanes, pa::kJoinY), dim3(256), 0, cs, 1, a);
@@ -1301,6 +1313,7 @@ extern "C" pa_status pa_window_attend(const pa_sessions* b, int32_t window, int3
   a.slots = l.slots;
   a.min_span = l.min_span;
   a.whole = l.whole;
+  a.give_up = pa_take_fault();
   a.lanes = l.lanes;
   a.scale_log2 = (softmax_scale != 0.f ? softmax_scale : 1.f / sqrtf((float)b->head_dim)) * pa::kLog2e;
   a.out = static_cast<uint16_t*>(out);

@@ -6,6 +6,8 @@ import math
 import pytest
 import torch
 
+from prefix_aware_decode_b200 import _binding
+
 import cache_ref as ref
 from cache_ref import Cache
 
@@ -260,3 +262,61 @@ def test_window_status_needs_no_workspace():
     ref.run_attend(c)
     s = torch.cuda.Stream()
     assert ref.pad.window_status() == ref.pad.window_status(device="cuda:0", stream=s) == ref.pad.PA_OK
+
+
+# Waits of the kernels that give up at once (pa_session_fault): the call ends, its status
+# says so, and the next one is clean.  (kv lengths, new rows, heads, the waits it comes to.)
+# Between them the cases come to every wait: 3 (a ring slot's last use) needs more blocks
+# a CTA than the ring holds, 1, 2, 4, 9 and 11 several items a CTA, 14 a block whose last
+# keys no row sees (a cut item has it in one CTA only, which may not hold a whole block)
+GIVE_UP = {
+    "two tiles": ([3000, 900], [300, 200], (8, 2, 128), [5, 6, 7, 8, 12, 13, 15]),
+    "one tile": ([20000], [3], (8, 2, 128), [3, 5, 6, 7, 10, 12, 13, 15, 16, 17]),
+    "short items": ([300 + 7 * i for i in range(90)], [5] * 90, (8, 8, 64), [1, 2, 4, 10, 11, 12, 14, 16, 17]),
+    "short items of two tiles": ([300 + 7 * i for i in range(40)], [290] * 40, (8, 8, 64), [1, 2, 4, 8, 9, 12, 15]),
+}
+
+
+@gpu
+@pytest.mark.parametrize("name,wait", [(n, w) for n, x in GIVE_UP.items() for w in x[3]])
+def test_attend_ends_when_a_wait_gives_up(name, wait):
+    kv, rows, heads, _ = GIVE_UP[name]
+    c = Cache(kv, rows, *heads, seed=101)
+    q, k, v, table, lens, cu = c.dev("q", "k", "v", "table", "lens", "cu")
+    ws = ref.pad.window_workspace(q, k, table, lens, cu)
+    want = ref.pad.window_attend(q, k, v, table, lens, cu, workspace=ws)
+    assert ref.pad.window_status(ws) == ref.pad.window_status() == ref.pad.PA_OK
+    assert _binding.lib().pa_session_fault(wait) == ref.pad.PA_OK
+    ref.pad.window_attend(q, k, v, table, lens, cu, workspace=ws)
+    assert ref.pad.window_status(ws) == ref.pad.PA_ERR_TIMEOUT
+    assert ref.pad.window_status() == ref.pad.PA_ERR_TIMEOUT
+    assert ref.pad.window_status() == ref.pad.PA_OK  # told once
+    got = ref.pad.window_attend(q, k, v, table, lens, cu, workspace=ws)
+    assert ref.pad.window_status(ws) == ref.pad.window_status() == ref.pad.PA_OK
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+WEIGH_GIVE_UP = {
+    "keys stream": ([5000 + 64 * i for i in range(20)], [1] * 20, (8, 8, 64), [1, 3, 4, 5, 6, 7, 8, 9, 10, 11, 13, 14]),
+    # 16 + 12 pairs of key blocks of 4 heads: one item a CTA, so no queue or K slot is used again (1, 4, 14)
+    "rows stream": ([4000, 3000], [1000, 900], (8, 4, 128), [3, 5, 6, 7, 8, 9, 10, 11, 12, 13]),
+}
+
+
+@gpu
+@pytest.mark.parametrize("name,wait", [(n, w) for n, x in WEIGH_GIVE_UP.items() for w in x[3]])
+def test_weigh_ends_when_a_wait_gives_up(name, wait):
+    kv, rows, heads, _ = WEIGH_GIVE_UP[name]
+    c = Cache(kv, rows, *heads, seed=102)
+    q, k, v, table, lens, cu = c.dev("q", "k", "v", "table", "lens", "cu")
+    _, lse = ref.pad.window_attend(q, k, v, table, lens, cu)
+    scores = [torch.zeros(len(kv), heads[1], c.width * 16, device="cuda") for _ in range(3)]
+    ref.pad.weigh_tokens(q, k, lse, table, lens, cu, scores[0])
+    assert ref.pad.weigh_status() == ref.pad.PA_OK
+    assert _binding.lib().pa_session_fault(wait) == ref.pad.PA_OK
+    ref.pad.weigh_tokens(q, k, lse, table, lens, cu, scores[1])
+    assert ref.pad.weigh_status() == ref.pad.PA_ERR_TIMEOUT
+    assert ref.pad.weigh_status() == ref.pad.PA_OK
+    ref.pad.weigh_tokens(q, k, lse, table, lens, cu, scores[2])
+    assert ref.pad.weigh_status() == ref.pad.PA_OK
+    assert torch.equal(scores[0], scores[2])
