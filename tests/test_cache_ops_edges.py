@@ -320,3 +320,56 @@ def test_weigh_ends_when_a_wait_gives_up(name, wait):
     ref.pad.weigh_tokens(q, k, lse, table, lens, cu, scores[2])
     assert ref.pad.weigh_status() == ref.pad.PA_OK
     assert torch.equal(scores[0], scores[2])
+
+
+# ------------------------------------------------------------------------------------------------ every page counts
+
+
+def _one_dim_a_page(c):
+    """V of a page is zero but in one dim, the page's index modulo D: an output dim is the
+    weight of a few pages, all of one sign, so that a page that is lost or taken for
+    another shows at any length (over random V a lost block of 128 keys disappears in the
+    bound of 20000)."""
+    g = torch.Generator().manual_seed(3)
+    for s, n in enumerate(c.kv):
+        for j in range(-(-n // 16)):
+            p = int(c.table[s, j])
+            if not 0 <= p < c.num_pages:
+                continue
+            c.v[p, :, :min(16, n - 16 * j)] = 0
+            c.v[p, :, :min(16, n - 16 * j), j % c.D] = (1 + torch.rand(1, generator=g)).bfloat16()
+    return c
+
+
+LONG = [([20011, 7], [1, 1], (4, 1, 128)), ([9000], [5], (4, 1, 128)), ([5000, 4097], [300, 17], (4, 2, 64)),
+        ([33000], [2], (8, 8, 64)), ([700] * 5, [1, 3, 1, 90, 1], (8, 2, 128)), ([1900, 1000], [1, 1], (8, 8, 128))]
+
+
+@gpu
+@pytest.mark.parametrize("kv,rows,heads", LONG)
+def test_attend_counts_every_page(kv, rows, heads):
+    c = _one_dim_a_page(Cache(kv, rows, *heads, seed=65))
+    out, _ = ref.run_attend(c)
+    want, tol = _attend(c)
+    ref.check(out, want, tol, "out")
+    out, _ = ref.run_attend(c, 1500, 40)
+    want, tol = _attend(c, 1500, 40)
+    ref.check(out, want, tol, "out")
+
+
+@pytest.mark.parametrize("kv,rows,heads", LONG[:2] + LONG[3:])
+def test_a_lost_or_swapped_page_is_outside_the_bound(kv, rows, heads):
+    g = torch.Generator().manual_seed(4)
+    c = _one_dim_a_page(Cache(kv, rows, *heads[:2], heads[2], seed=65, device="cpu"))
+    want, tol = _attend(c)
+    n = -(-kv[0] // 16) - 1
+    for j in [0, n - 1] + torch.randint(0, n, (2,), generator=g).tolist():
+        p, other = int(c.table[0, j]), int(c.table[0, (j + 1) % n])
+        held = c.v.clone()
+        for lost in (True, False):
+            c.v[p] = 0 if lost else held[other]
+            got, _ = _attend(c)
+            c.v.copy_(held)
+            row = slice(0, rows[0])
+            bad = ((got - want).abs() > tol)[row].any(dim=2)
+            assert bool(bad.all()), (j, lost)  # in every row and head
