@@ -971,7 +971,9 @@ __global__ void __launch_bounds__(256) window_join_kernel(const AttendArgs a) {
 //   256 x 400-900, 32/8x128       124.3  149.3       256 x 1200-1900, 8/4x128    132.6 143.5 (6.1 TB/s)
 // Past the rule the other wins: 64 x 1500-2000, 32/8x128: 89.5 and 85.7 us; 64 x
 // 3000-4000: 169 and 153 us; 256 x 100-900, 64/8x128: 142.8 and 137.3 us; 4 rows a
-// session, each a read of the same pages, 16 x 500-900: 39.6 and 23.8 us.
+// session, each a read of the same pages, 16 x 500-900: 39.6 and 23.8 us.  The rows are
+// counted on average, since the host does not know them one by one: a chunk of 64 rows
+// over 800 tokens among 63 single rows, 32/8x128: 54.5 and 51.6 us.
 constexpr int kShortPages = 128;
 constexpr int kShortCluster = 8;
 constexpr int kShortThreads = 256, kShortWarps = kShortThreads / 32;

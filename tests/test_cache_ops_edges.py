@@ -373,3 +373,19 @@ def test_a_lost_or_swapped_page_is_outside_the_bound(kv, rows, heads):
             row = slice(0, rows[0])
             bad = ((got - want).abs() > tol)[row].any(dim=2)
             assert bool(bad.all()), (j, lost)  # in every row and head
+
+
+# ------------------------------------------------------------------------------------------------ a long chunk among single rows
+
+
+@gpu
+@pytest.mark.parametrize("heads", [(8, 2, 128), (8, 8, 64), (8, 1, 64)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (60, 9)])
+def test_attend_one_long_chunk_among_single_rows(heads, window, sinks):
+    # few rows a session on average: the form for few rows also takes the session with many
+    rows = [1] * 30 + [25, 0, 0, 1]
+    kv = [40 + 17 * i for i in range(30)] + [300, 50, 0, 90]
+    c = Cache(kv, rows, *heads, seed=97)
+    out, _ = ref.run_attend(c, window, sinks)
+    want, tol = _attend(c, window, sinks)
+    ref.check(out, want, tol, "out")
