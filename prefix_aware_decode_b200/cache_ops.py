@@ -128,7 +128,9 @@ def evict_tokens(scores, k_pool, v_pool, block_table, kv_lens, dst_table, budget
     """Keeps, per (session, kv head), the first `sinks`, the last `recent` and the
     highest-scoring other tokens, `budget` in all, and copies their K and V in
     order to the pages of dst_table int32 [S][n] (pa_evict_tokens; pages that no
-    row of block_table names; a kept token in a hole becomes one of zeros).  Returns (new_lens int32 [S], kept int32
+    row of block_table names, as SessionPool.compact and then tables(sessions,
+    max_pages=the budget's pages) give them; n pages hold the budget; a kept
+    token in a hole becomes one of zeros).  Returns (new_lens int32 [S], kept int32
     [S][Hkv][budget] former indices then -1, scores_out fp32 [S][Hkv][max_tokens])."""
     if stream is not None:
         with _on(stream, k_pool.device):

@@ -11,7 +11,8 @@ builds the decode batch of every registered query for the planner
 
 It moves no data: appends and forks return the page slots the caller writes
 new K/V into (rope_append writes them from `tables`), and the page copies a fork
-needs; `compact` gives the pages that an eviction copies the kept tokens to.
+needs; `compact` gives the pages that an eviction copies the kept tokens to (as a
+table: `tables` with the budget's pages as its width).
 The device pools stay the caller's.  Shared pages are reference-counted and go back to the free list
 when no session holds them.
 """
@@ -174,12 +175,18 @@ class SessionPool:
             kv[i] = s.n_tokens
         return [q for _, q in rows], [sid for sid, _ in rows], bt, kv
 
-    def tables(self, sessions=None):
+    def tables(self, sessions=None, max_pages=None):
         """One row per session (all of them, by id, by default), as the
         session-cache operators take them: block_table int32 [S][max_pages] with -1
-        past the pages, and kv_lens int32 [S]."""
+        past the pages, and kv_lens int32 [S].  max_pages: the table's width (that of
+        the longest session by default), for a table that a captured graph keeps as
+        sessions grow, or for evict_tokens' dst_table (the budget's pages, after
+        compact).  ValueError when a session has more pages."""
         sids = sorted(self._sessions) if sessions is None else list(sessions)
-        width = max([len(self._sessions[sid].pages) for sid in sids] + [1])
+        longest = max([len(self._sessions[sid].pages) for sid in sids] + [1])
+        width = longest if max_pages is None else int(max_pages)
+        if width < longest:
+            raise ValueError(f"a table of {width} pages is narrower than a session of {longest}")
         bt = np.full((len(sids), width), -1, dtype=np.int32)
         for i, sid in enumerate(sids):
             bt[i, :len(self._sessions[sid].pages)] = self._sessions[sid].pages

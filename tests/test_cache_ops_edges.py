@@ -7,6 +7,7 @@ import pytest
 import torch
 
 from prefix_aware_decode_b200 import _binding
+from prefix_aware_decode_b200.session import SessionPool
 
 import cache_ref as ref
 from cache_ref import Cache
@@ -389,3 +390,43 @@ def test_attend_one_long_chunk_among_single_rows(heads, window, sinks):
     out, _ = ref.run_attend(c, window, sinks)
     want, tol = _attend(c, window, sinks)
     ref.check(out, want, tol, "out")
+
+
+# ------------------------------------------------------------------------------------------------ tables
+
+
+def test_session_pool_tables_of_a_given_width():
+    pool = SessionPool(40)
+    for s, n in enumerate([100, 0, 17]):
+        pool.open(s)
+        pool.append(s, n)
+    table, lens = pool.tables(max_pages=9)
+    assert table.shape == (3, 9) and table.dtype == "int32" and lens.tolist() == [100, 0, 17]
+    narrow, _ = pool.tables()
+    assert (table[:, :7] == narrow).all() and (table[:, 7:] == -1).all()
+    assert pool.tables([1], max_pages=1)[0].tolist() == [[-1]]
+    for bad in (6, 0, -1):
+        with pytest.raises(ValueError):
+            pool.tables(max_pages=bad)
+
+
+@gpu
+def test_evict_into_the_pages_that_the_pool_gives():
+    # every session shorter than the budget: its table is narrower than the budget's pages
+    pool = SessionPool(40)
+    for s, n in enumerate([37, 20]):
+        pool.open(s)
+        pool.append(s, n)
+    budget = 64
+    table, lens = (torch.from_numpy(t).cuda() for t in pool.tables())
+    kp = torch.randn(40, 2, 16, 64, device="cuda").bfloat16()
+    vp = torch.randn_like(kp)
+    old = kp.clone()
+    pool.compact([0, 1], budget)
+    dst, want = pool.tables(max_pages=budget // 16)
+    scores = torch.rand(2, 2, 64, device="cuda")
+    new, kept, _ = ref.pad.evict_tokens(scores, kp, vp, table, lens, torch.from_numpy(dst).cuda(), budget)
+    assert new.tolist() == want.tolist() == [37, 20]
+    for s in range(2):
+        for t in range(int(new[s])):
+            assert torch.equal(kp[int(dst[s, t // 16]), :, t % 16], old[int(table[s, t // 16]), :, t % 16])
