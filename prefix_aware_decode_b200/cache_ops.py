@@ -10,7 +10,8 @@ into a CUDA graph and replayed as the lengths and tables change in place.
 All tensors of a call live on one device, which need not be the current one.
 A call runs on `stream` (a torch stream of that device, or a cudaStream_t), or on
 the device's current stream; outputs and workspaces that it allocates belong to
-that stream.  Argument errors raise ValueError (TypeError for what is no tensor),
+that stream.  There is no backward: tensors that require grad are refused unless
+grad mode is off.  Argument errors raise ValueError (TypeError for what is no tensor),
 errors of the library PaError.
 """
 from __future__ import annotations

@@ -32,11 +32,23 @@ const char* type_name(at::ScalarType t) {
   return t == at::kBFloat16 ? "bfloat16" : t == at::kFloat ? "float32" : t == at::kDouble ? "float64" : t == at::kInt ? "int32" : "uint8";
 }
 
+// These operators have no backward: a result that silently left the graph would be wrong.
+void no_grad(const Tensor& t, const char* name) {
+  if (t.requires_grad() && at::GradMode::is_enabled())
+    bad(std::string(name) + " requires grad, and this operator has no backward: call it under torch.no_grad()");
+}
+
+// A tensor that a call has changed in place counts a version, as torch's own do.
+void changed(const Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // Address of a contiguous tensor of one type on CUDA device `index`.
 void* ptr(const Tensor& t, const char* name, at::ScalarType type, c10::DeviceIndex index, uintptr_t align) {
   if (!t.defined() || t.scalar_type() != type) bad(std::string(name) + " must be a " + type_name(type) + " tensor");
   if (!t.is_cuda() || t.get_device() != index) bad(std::string(name) + " must be on the pools' device");
   if (!t.is_contiguous()) bad(std::string(name) + " must be contiguous");
+  no_grad(t, name);
   void* p = t.data_ptr();
   if (reinterpret_cast<uintptr_t>(p) % align) bad(std::string(name) + " must be " + std::to_string(align) + "-byte aligned");
   return p;
@@ -95,6 +107,7 @@ const void* strided(const Tensor& t, const char* name, int64_t rows, int64_t hea
     bad(std::string(name) + " must be a bf16 tensor [" + std::to_string(rows) + "][" + std::to_string(heads) + "][" +
         std::to_string(D) + "]");
   if (!t.is_cuda() || t.get_device() != index) bad(std::string(name) + " must be on the pools' device");
+  no_grad(t, name);
   if ((D > 1 && t.stride(2) != 1) || (heads > 1 && t.stride(1) != D))
     bad(std::string(name) + ": the heads of a row must be contiguous");
   *stride = rows > 1 ? t.stride(0) : heads * D;
@@ -154,6 +167,9 @@ Tensor rope_append(const Tensor& q, const Tensor& k, const Tensor& v, const Tens
   void* op;
   Tensor out = output(q_out, "q_out", {rows, Hq, D}, at::kBFloat16, index, 16, &op);
   check(pa_rope_append(&b, &r, qp, qs, kp, ks, vp, vs, kpool, vpool, op, current(index)), "pa_rope_append");
+  changed(out);
+  changed(k_pool);
+  changed(v_pool);
   return out;
 }
 
@@ -193,6 +209,8 @@ std::tuple<Tensor, Tensor> window_attend(const Tensor& q, const Tensor& k_pool, 
   check(pa_window_attend(&b, i32(window, "window"), i32(sinks, "sinks"), (float)scale, qp, kp, vp, wp, ws.numel(), op,
                          static_cast<float*>(lp), current(index)),
         "pa_window_attend");
+  changed(o);
+  changed(l);
   return {o, l};
 }
 
@@ -230,6 +248,7 @@ Tensor weigh_tokens(const Tensor& q, const Tensor& k_pool, const Tensor& lse, co
   check(pa_weigh_tokens(&b, i32(window, "window"), i32(sinks, "sinks"), (float)scale, qp, kp,
                         static_cast<const float*>(lp), static_cast<float*>(sp), scores.size(2), current(index)),
         "pa_weigh_tokens");
+  changed(scores);
   return scores;
 }
 
@@ -269,6 +288,9 @@ std::tuple<Tensor, Tensor, Tensor> evict_tokens(const Tensor& scores, const Tens
                         i32(recent, "recent"), static_cast<float*>(xp), kept.data_ptr<int32_t>(),
                         lens.data_ptr<int32_t>(), current(index)),
         "pa_evict_tokens");
+  changed(x);
+  changed(k_pool);
+  changed(v_pool);
   return {lens, kept, x};
 }
 

@@ -430,3 +430,64 @@ def test_evict_into_the_pages_that_the_pool_gives():
     for s in range(2):
         for t in range(int(new[s])):
             assert torch.equal(kp[int(dst[s, t // 16]), :, t % 16], old[int(table[s, t // 16]), :, t % 16])
+
+
+# ------------------------------------------------------------------------------------------------ autograd
+
+
+@gpu
+def test_tensors_that_require_grad_are_refused():
+    c = Cache([20, 5], [2, 1], 8, 2, 64, seed=98)
+    q, k, v, table, lens, cu = c.dev("q", "k", "v", "table", "lens", "cu")
+    out, lse = ref.pad.window_attend(q, k, v, table, lens, cu)
+    scores = torch.zeros(2, 2, 64, device="cuda")
+    pos, inv = torch.zeros(3).int().cuda(), torch.ones(32, dtype=torch.float64, device="cuda")
+    kv = torch.zeros(3, 2, 64, device="cuda").bfloat16()
+    dst = torch.full((2, 4), -1).int().cuda()
+
+    def grad(t):
+        return t.clone().requires_grad_()
+
+    calls = [lambda: ref.pad.window_attend(grad(q), k, v, table, lens, cu),
+             lambda: ref.pad.window_attend(q, grad(k), v, table, lens, cu),
+             lambda: ref.pad.window_attend(q, k, grad(v), table, lens, cu),
+             lambda: ref.pad.window_attend(q, k, v, table, lens, cu, out=grad(out)),
+             lambda: ref.pad.weigh_tokens(grad(q), k, lse, table, lens, cu, scores),
+             lambda: ref.pad.weigh_tokens(q, k, grad(lse), table, lens, cu, scores),
+             lambda: ref.pad.weigh_tokens(q, k, lse, table, lens, cu, grad(scores)),
+             lambda: ref.pad.rope_append(grad(q), kv, kv, pos, inv, k, v, table, lens, cu),
+             lambda: ref.pad.rope_append(q, kv, grad(kv), pos, inv, k, v, table, lens, cu),
+             lambda: ref.pad.evict_tokens(grad(scores), k, v, table, lens, dst, 32)]
+    for i, call in enumerate(calls):
+        with pytest.raises(ValueError, match="grad"):
+            call()
+    with torch.no_grad():  # no graph is asked for
+        o, _ = ref.pad.window_attend(grad(q), k, v, table, lens, cu)
+    assert torch.equal(o, out)
+    with torch.inference_mode():
+        o, _ = ref.pad.window_attend(q, k, v, table, lens, cu)
+        ref.pad.weigh_tokens(q, k, lse, table, lens, cu, torch.zeros_like(scores))
+    assert torch.equal(o, out)
+
+
+@gpu
+def test_tensors_that_a_call_changes_count_a_version():
+    c = Cache([20, 5], [2, 1], 8, 2, 64, seed=99)
+    q, k, v, table, lens, cu = c.dev("q", "k", "v", "table", "lens", "cu")
+    scores = torch.zeros(2, 2, 64, device="cuda")
+    pos, inv = torch.zeros(3).int().cuda(), torch.ones(32, dtype=torch.float64, device="cuda")
+    kv = torch.zeros(3, 2, 64, device="cuda").bfloat16()
+    out, lse = ref.pad.window_attend(q, k, v, table, lens, cu)
+    x = torch.zeros_like(scores)
+    dst = torch.full((2, 4), -1).int().cuda()
+
+    def grows(call, *changed, same=()):
+        before = [t._version for t in changed], [t._version for t in same]
+        call()
+        assert all(t._version > n for t, n in zip(changed, before[0])), "a changed tensor kept its version"
+        assert [t._version for t in same] == before[1]
+
+    grows(lambda: ref.pad.window_attend(q, k, v, table, lens, cu, out=out, lse=lse), out, lse, same=(q, k, v))
+    grows(lambda: ref.pad.weigh_tokens(q, k, lse, table, lens, cu, scores), scores, same=(q, k, lse))
+    grows(lambda: ref.pad.rope_append(q, kv, kv, pos, inv, k, v, table, lens, cu, q_out=q), q, k, v, same=(kv,))
+    grows(lambda: ref.pad.evict_tokens(scores, k, v, table, lens, dst, 32, scores_out=x), k, v, x, same=(scores,))
