@@ -8,6 +8,8 @@ version another package in the process brings.
 """
 from __future__ import annotations
 
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -20,6 +22,7 @@ INCLUDE = os.path.join(REPO, "include")
 BUILD = os.path.join(REPO, "_build")
 LIB = os.path.join(HERE, "libpa.so")
 TORCH_OPS = os.path.join(HERE, "_cache_ops.so")
+STAMP = os.path.join(BUILD, "_cache_ops.made_for")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 CU_SOURCES = ["kernels.cu", "capi.cu", "noalloc.cu", "rope_append.cu", "window_attend.cu", "weigh.cu", "evict.cu"]
@@ -39,6 +42,13 @@ def _newer(target: str, deps) -> bool:
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _read(path: str) -> str:
+    if not os.path.exists(path):
+        return ""
+    with open(path) as f:
+        return f.read()
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -68,16 +78,28 @@ def build(force: bool = False, verbose: bool = False) -> str:
     return LIB
 
 
-def build_torch_ops(force: bool = False, verbose: bool = False) -> str:
+def build_torch_ops(force: bool = False, verbose: bool = False):
     """The Python module _cache_ops (csrc/torch_ops.cpp), against the installed
-    torch; libpa.so is found beside it ($ORIGIN)."""
+    torch; libpa.so is found beside it ($ORIGIN).  Without torch or its headers it is
+    left out (None), with a line on stderr: the C ABI and the planned path need
+    neither.  Built anew for another torch or Python than it was built for."""
+    try:
+        version = importlib.metadata.version("torch")
+        root = os.path.dirname(importlib.util.find_spec("torch").origin)
+    except (importlib.metadata.PackageNotFoundError, AttributeError):
+        root = None
+    if root is None or not os.path.isdir(os.path.join(root, "include", "torch")):
+        print("torch or its headers are not installed: _cache_ops.so (the session-cache operators on torch tensors) "
+              "is not built", file=sys.stderr)
+        return None
+    made_for = f"torch {version} python {sys.version}"
     src = os.path.join(CSRC, "torch_ops.cpp")
-    if not (force or _newer(TORCH_OPS, [src, os.path.join(INCLUDE, "pa.h")])):
+    os.makedirs(BUILD, exist_ok=True)
+    if not (force or _newer(TORCH_OPS, [src, os.path.join(INCLUDE, "pa.h")]) or _read(STAMP) != made_for):
         return TORCH_OPS
     import sysconfig
 
     import torch
-    root = os.path.dirname(torch.__file__)
     abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
     tmp = TORCH_OPS + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
@@ -90,6 +112,8 @@ def build_torch_ops(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.check_call(cmd)
     os.replace(tmp, TORCH_OPS)
+    with open(STAMP, "w") as f:
+        f.write(made_for)
     return TORCH_OPS
 
 
