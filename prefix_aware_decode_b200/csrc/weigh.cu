@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = Shape<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023) {  // the swizzle needs it; the kernel has no other shared memory before it
+    griddep_wait();  // a launch ends no earlier than those before it on the stream
     if (threadIdx.x == 0) record_status(g_weigh_status, PA_ERR_DEVICE, blockIdx.x, 0);
     return;
   }
