@@ -445,7 +445,7 @@ pa_status pa_window_workspace_size(const pa_sessions *b, int32_t window, int32_t
  * and sinks.  The row at position p sees token t when t <= p and
  * (window == 0 or t > p - window or t < sinks).
  *   window, sinks     >= 0; window 0: no limit
- *   softmax_scale     > 0, finite; 0 selects 1 / sqrt(D)
+ *   softmax_scale     > 0, at most 2.3e38; 0 selects 1 / sqrt(D)
  *   q                 device bf16 [num_rows][Hq][D]
  *   out               device bf16 [num_rows][Hq][D]
  *   lse               device fp32 [num_rows][Hq], natural log; may be NULL

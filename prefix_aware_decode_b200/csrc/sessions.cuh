@@ -93,6 +93,10 @@ inline pa::Window pa_window(int32_t window, int32_t sinks) {
   return pa::Window{window < most ? window : most, sinks < most ? sinks : most};
 }
 
+// A softmax scale whose product with log2 e, which the kernels scale by, is finite too
+// (0 times an infinity would be NaN).
+inline bool pa_scale_ok(float scale) { return scale >= 0.f && scale <= 2.3e38f; }
+
 // Checks of a pa_sessions that every operator makes.  `rows`: the
 // operator uses the rows of the batch (cu_rows).
 inline pa_status pa_check_sessions(const pa_sessions* b, bool rows) {

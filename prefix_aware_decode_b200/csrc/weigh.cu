@@ -644,7 +644,7 @@ extern "C" pa_status pa_weigh_tokens(const pa_sessions* b, int32_t window, int32
                                      int64_t max_tokens, void* stream) {
   const pa_status st = pa_check_sessions(b, true);
   if (st != PA_OK) return st;
-  if (window < 0 || sinks < 0 || max_tokens < 1 || !scores || !(softmax_scale >= 0.f) || softmax_scale > 3.4e38f)
+  if (window < 0 || sinks < 0 || max_tokens < 1 || !scores || !pa_scale_ok(softmax_scale))
     return PA_ERR_INVALID;
   if (b->num_rows == 0) return PA_OK;
   if (!q || !k_pool || !lse || !pa_aligned16(q) || !pa_aligned16(k_pool)) return PA_ERR_INVALID;

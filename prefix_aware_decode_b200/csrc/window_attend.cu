@@ -1294,7 +1294,7 @@ extern "C" pa_status pa_window_attend(const pa_sessions* b, int32_t window, int3
                                       size_t workspace_bytes, void* out, float* lse, void* stream) {
   const pa_status st = pa_check_sessions(b, true);
   if (st != PA_OK) return st;
-  if (window < 0 || sinks < 0 || !(softmax_scale >= 0.f) || softmax_scale > 3.4e38f) return PA_ERR_INVALID;
+  if (window < 0 || sinks < 0 || !pa_scale_ok(softmax_scale)) return PA_ERR_INVALID;
   pa::Launch l;
   if (!pa::plan_launch(*b, pa_window(window, sinks), &l)) return PA_ERR_UNSUPPORTED;
   if (b->num_rows == 0) {  // nothing but the status of a workspace that is given

@@ -491,3 +491,14 @@ def test_tensors_that_a_call_changes_count_a_version():
     grows(lambda: ref.pad.weigh_tokens(q, k, lse, table, lens, cu, scores), scores, same=(q, k, lse))
     grows(lambda: ref.pad.rope_append(q, kv, kv, pos, inv, k, v, table, lens, cu, q_out=q), q, k, v, same=(kv,))
     grows(lambda: ref.pad.evict_tokens(scores, k, v, table, lens, dst, 32, scores_out=x), k, v, x, same=(scores,))
+
+
+# ------------------------------------------------------------------------------------------------ scale
+
+
+def test_a_scale_whose_multiple_by_log2_e_overflows_is_refused():
+    b = _binding.PaSessions(2, 3, 8, 2, 64, 16, 4, 9, 4096, 8192, 12288)
+    p, L = 1 << 20, _binding.lib()
+    for scale in (2.4e38, 3.4e38, math.inf):
+        assert L.pa_window_attend(b, 0, 0, scale, p, p, p, p, 1 << 30, p, p, None) == _binding.PA_ERR_INVALID
+        assert L.pa_weigh_tokens(b, 0, 0, scale, p, p, p, p, 64, None) == _binding.PA_ERR_INVALID
