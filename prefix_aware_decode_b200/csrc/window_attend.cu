@@ -573,13 +573,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = wwait(mi.p_full[1], c1, 8))) break;
           ++c1;
           issue_o(1, pv % S::NS, pages, j == 0, false);
+          commit(mi.empty[pv % S::NS]);
           if (more) {
             issue_s(1, 1, pk % S::NS);
-            commit(mi.empty[pv % S::NS]);
             commit(mi.empty[pk % S::NS]);
             if (j + 2 == n) commit(mi.q_empty);
           } else {
-            commit(mi.empty[pv % S::NS]);
             commit(mi.o_full[1]);
           }
         }
@@ -599,14 +598,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait_load(pv) && (j || it == 0 || wwait(mi.o_free, it - 1, 11)) && wwait(mi.p_full[tile], phase, 10);
           if (!ok) break;
           issue_o(tile, pv % S::NS, pages, j < 2, twin);
-          if (more && !(ok = wait_load(pk))) break;
+          commit(mi.empty[pv % S::NS]);
           if (more) {
+            if (!(ok = wait_load(pk))) break;
             issue_s(tile, 0, pk % S::NS);
-            commit(mi.empty[pv % S::NS]);
             commit(mi.empty[pk % S::NS]);
             if (j + 3 == n) commit(mi.q_empty);
           } else {
-            commit(mi.empty[pv % S::NS]);
             commit(mi.o_full[tile]);
           }
         }
@@ -653,114 +651,115 @@ __global__ void __launch_bounds__(kThreads, 1)
       int page_next = page_of(pair ? 0 : grp);
       float m = -INFINITY, l = 0.f;
       bool first = true;
-      for (int j = pair ? 0 : grp; j < n && ok; j += pair ? 1 : 2) {
-        const int v0 = 8 * (b0 + j), pages = min(8, t.np - v0);
-        const unsigned holes = __ballot_sync(0xffffffffu, page_next < 0);
-        page_next = page_of(j + (pair ? 1 : 2));
-        const int t_first = t.page_index(v0) * kPage, t_last = t.page_index(v0 + pages - 1) * kPage + kPage - 1;
-        const bool all = pages == 8 && holes == 0 && t_last <= p_min &&
-                         (a.w.window == 0 || (v0 >= t.ns && t_first > p_max - a.w.window) || t_last < a.w.sinks);
-        // tokens that no row of the item sees (past the session's end, between the
-        // sinks and the first window) may hold anything: a weight of 0 times NaN is
-        // NaN, so their V rows are zeroed; the first tile of a pair does it for both
-        bool dead = false;
-        if (!all && lane < pages) {
-          const int t0 = t.page_index(v0 + lane) * kPage;
-          dead = t0 + kPage > kv_end || (t0 + kPage > a.w.sinks && t0 < seen_from);
-        }
-        if (!(ok = wwait(mi.s_full[grp], ps++, 13))) break;
-        tc_fence_after();
-        if (__any_sync(0xffffffffu, dead) && (grp == 0 || !pair)) {
-          const int pv = pos_v(base, j, n);
-          // (after the block's scores: the slot's last use is then over, which the
-          // parity of a phase alone would not tell)
-          if (!(ok = wwait(mi.full[pv % S::NS], pv / S::NS, 14))) break;
-          const int key = tid & 127, tk0 = t.page_index(v0 + (key >> 4)) * kPage + (key & 15);
-          if ((key >> 4) < pages && (tk0 >= kv_end || (tk0 >= a.w.sinks && tk0 < seen_from))) {
-            uint8_t* vt = ring + (pv % S::NS) * S::TILE + key * 128;
-#pragma unroll
-            for (int i = 0; i < 8 * S::HALVES; ++i)
-              *reinterpret_cast<uint4*>(vt + (i >> 3) * S::BLK + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+      // (two copies: in one the registers of both ways are live, prompt chunk 2.7 and 2.57 ms)
+      auto walk = [&](auto twin_tag) {
+        constexpr bool TWIN = decltype(twin_tag)::value;
+        for (int j = pair ? 0 : grp; j < n && ok; j += pair ? 1 : 2) {
+          const int v0 = 8 * (b0 + j), pages = min(8, t.np - v0);
+          const unsigned holes = __ballot_sync(0xffffffffu, page_next < 0);
+          page_next = page_of(j + (pair ? 1 : 2));
+          const int t_first = t.page_index(v0) * kPage, t_last = t.page_index(v0 + pages - 1) * kPage + kPage - 1;
+          const bool all = pages == 8 && holes == 0 && t_last <= p_min &&
+                           (a.w.window == 0 || (v0 >= t.ns && t_first > p_max - a.w.window) || t_last < a.w.sinks);
+          // tokens that no row of the item sees (past the session's end, between the
+          // sinks and the first window) may hold anything: a weight of 0 times NaN is
+          // NaN, so their V rows are zeroed; the first tile of a pair does it for both
+          bool dead = false;
+          if (!all && lane < pages) {
+            const int t0 = t.page_index(v0 + lane) * kPage;
+            dead = t0 + kPage > kv_end || (t0 + kPage > a.w.sinks && t0 < seen_from);
           }
-          fence_proxy_async_smem();
-        }
-        // none of the tile's rows sees a key of the block: all weights are 0
-        const bool none = t_first > p_max || (a.w.window != 0 && v0 >= t.ns && t_last <= p_min - a.w.window &&
-                                              t_first >= a.w.sinks);
-        if (!busy || none) {
-          if (busy) {
-            float z[32];
+          if (!(ok = wwait(mi.s_full[grp], ps++, 13))) break;
+          tc_fence_after();
+          if (__any_sync(0xffffffffu, dead) && (grp == 0 || !pair)) {
+            const int pv = pos_v(base, j, n);
+            // (after the block's scores: the slot's last use is then over, which the
+            // parity of a phase alone would not tell)
+            if (!(ok = wwait(mi.full[pv % S::NS], pv / S::NS, 14))) break;
+            const int key = tid & 127, tk0 = t.page_index(v0 + (key >> 4)) * kPage + (key & 15);
+            if ((key >> 4) < pages && (tk0 >= kv_end || (tk0 >= a.w.sinks && tk0 < seen_from))) {
+              uint8_t* vt = ring + (pv % S::NS) * S::TILE + key * 128;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) z[i] = 0.f;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_st32(t_s + 32 * c, z);
-            tmem_wait_st();
+              for (int i = 0; i < 8 * S::HALVES; ++i)
+                *reinterpret_cast<uint4*>(vt + (i >> 3) * S::BLK + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(mi.p_full[grp]));
-          continue;
-        }
-        float x[4][32];
+          // none of the tile's rows sees a key of the block: all weights are 0
+          const bool none = t_first > p_max || (a.w.window != 0 && v0 >= t.ns && t_last <= p_min - a.w.window &&
+                                                t_first >= a.w.sinks);
+          if (!busy || none) {
+            if (busy) {
+              float z[32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, x[c]);
+              for (int i = 0; i < 32; ++i) z[i] = 0.f;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_wait_ld_into(x[c]);
-        if (!all) {
+              for (int c = 0; c < 4; ++c) tmem_st32(t_s + 32 * c, z);
+              tmem_wait_st();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(mi.p_full[grp]));
+            continue;
+          }
+          float x[4][32];
 #pragma unroll
-          for (int pg = 0; pg < 8; ++pg) {
-            const int t0 = t.page_index(v0 + pg) * kPage;
-            const bool gone = pg >= pages || (holes >> pg & 1);
-            // bit i: this row sees token t0 + i
-            const int top = p - t0, under = a.w.window ? p - a.w.window - t0 : -1, sk = a.w.sinks - t0;
-            const uint32_t upto = top < 0 ? 0u : 0xffffu >> (15 - min(top, 15));
-            const uint32_t from = under < 0 ? 0xffffu : 0xffffu << min(under + 1, 16);
-            const uint32_t sink = sk <= 0 ? 0u : 0xffffu >> (16 - min(sk, 16));
-            const uint32_t see = gone ? 0u : upto & (from | sink);
-            if (__any_sync(0xffffffffu, see != 0xffffu)) {
+          for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, x[c]);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float& y = x[pg >> 1][16 * (pg & 1) + i];
-                y = see & (1u << i) ? y : -INFINITY;
+          for (int c = 0; c < 4; ++c) tmem_wait_ld_into(x[c]);
+          if (!all) {
+#pragma unroll
+            for (int pg = 0; pg < 8; ++pg) {
+              const int t0 = t.page_index(v0 + pg) * kPage;
+              const bool gone = pg >= pages || (holes >> pg & 1);
+              // bit i: this row sees token t0 + i
+              const int top = p - t0, under = a.w.window ? p - a.w.window - t0 : -1, sk = a.w.sinks - t0;
+              const uint32_t upto = top < 0 ? 0u : 0xffffu >> (15 - min(top, 15));
+              const uint32_t from = under < 0 ? 0xffffu : 0xffffu << min(under + 1, 16);
+              const uint32_t sink = sk <= 0 ? 0u : 0xffffu >> (16 - min(sk, 16));
+              const uint32_t see = gone ? 0u : upto & (from | sink);
+              if (__any_sync(0xffffffffu, see != 0xffffu)) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  float& y = x[pg >> 1][16 * (pg & 1) + i];
+                  y = see & (1u << i) ? y : -INFINITY;
+                }
               }
             }
           }
-        }
-        float mq[4];
+          float mq[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mq[c] = x[c][0];
+          for (int c = 0; c < 4; ++c) {
+            mq[c] = x[c][0];
 #pragma unroll
-          for (int i = 1; i < 31; i += 2) mq[c] = max3(mq[c], x[c][i], x[c][i + 1]);
-        }
-        float mx = max3(max3(mq[0], mq[1], x[0][31]), max3(mq[2], mq[3], x[1][31]), fmaxf(x[2][31], x[3][31]));
-        if (twin) mx = __shfl_sync(0xffffffffu, mx, lane & 15);  // both lanes of a row rescale alike
-        mx *= a.scale_log2;
-        if (first) {
-          m = mx;
-        } else if (__any_sync(0xffffffffu, mx > m + kRaise)) {
-          const float mn = mx > m + kRaise ? mx : m;
-          const float f = mn == -INFINITY ? 1.f : ex2(m - mn);  // O and l are 0 while m is -inf
-          l *= f;
-          m = mn;
+            for (int i = 1; i < 31; i += 2) mq[c] = max3(mq[c], x[c][i], x[c][i + 1]);
+          }
+          float mx = max3(max3(mq[0], mq[1], x[0][31]), max3(mq[2], mq[3], x[1][31]), fmaxf(x[2][31], x[3][31]));
+          if (TWIN) mx = __shfl_sync(0xffffffffu, mx, lane & 15);  // both lanes of a row rescale alike
+          mx *= a.scale_log2;
+          if (first) {
+            m = mx;
+          } else if (__any_sync(0xffffffffu, mx > m + kRaise)) {
+            const float mn = mx > m + kRaise ? mx : m;
+            const float f = mn == -INFINITY ? 1.f : ex2(m - mn);  // O and l are 0 while m is -inf
+            l *= f;
+            m = mn;
 #pragma unroll 1
-          for (int c = 0; c < D; c += 8) tmem_scale8(t_o + c, f);
-          tmem_wait_st();
-        }
-        first = false;
-        const float mc = m == -INFINITY ? 0.f : -m;
-        const float2 sc = make_float2(a.scale_log2, a.scale_log2), mm = make_float2(mc, mc);
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // the weights, 32 keys at a time
-        auto cut = [](float2 y) {  // to bf16
-          return make_float2(__uint_as_float(__float_as_uint(y.x) & 0xffff0000u),
-                             __uint_as_float(__float_as_uint(y.y) & 0xffff0000u));
-        };
-        const float2 neg = make_float2(-1.f, -1.f);
-        // of a row in two lanes: y cut, or what that leaves
-        const float2 fy = low ? make_float2(1.f, 1.f) : make_float2(0.f, 0.f), fc = low ? neg : make_float2(1.f, 1.f);
-        auto weights = [&](auto twin_tag) {
-          constexpr bool TWIN = decltype(twin_tag)::value;
+            for (int c = 0; c < D; c += 8) tmem_scale8(t_o + c, f);
+            tmem_wait_st();
+          }
+          first = false;
+          const float mc = m == -INFINITY ? 0.f : -m;
+          const float2 sc = make_float2(a.scale_log2, a.scale_log2), mm = make_float2(mc, mc);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          // the weights, 32 keys at a time
+          auto cut = [](float2 y) {  // to bf16
+            return make_float2(__uint_as_float(__float_as_uint(y.x) & 0xffff0000u),
+                               __uint_as_float(__float_as_uint(y.y) & 0xffff0000u));
+          };
+          const float2 neg = make_float2(-1.f, -1.f);
+          // of a row in two lanes: y cut, or what that leaves
+          const float2 fy = low ? make_float2(1.f, 1.f) : make_float2(0.f, 0.f), fc = low ? neg : make_float2(1.f, 1.f);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             float pw[32];
@@ -782,15 +781,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (TWIN) tmem_st16<0>(t_s + 16 * c, pw);
             else tmem_st32(t_s + 32 * c, pw);
           }
-        };
-        if (twin) weights(std::true_type{});
-        else weights(std::false_type{});
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(mi.p_full[grp]));
-        l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
-      }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(mi.p_full[grp]));
+          l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+        }
+      };
+      if (twin) walk(std::true_type{});
+      else walk(std::false_type{});
       if (!ok) break;
       // ---------------- the item's end
       const int n_mine = pair ? n : (n - grp + 1) >> 1;  // blocks of this group
