@@ -508,10 +508,10 @@ pa_status pa_evict_tokens(const pa_sessions *b, const float *scores, int64_t max
                           const int32_t *d_dst_table, int32_t dst_max_pages, int32_t budget, int32_t sinks,
                           int32_t recent, float *scores_out, int32_t *kept, int32_t *new_lens, void *stream);
 
-/* Tests only: in this thread's next pa_window_attend or pa_weigh_tokens call the
- * device-side waits of number `wait` (0: none) give up at once, as they would after
- * their limit: the call ends with PA_ERR_TIMEOUT in its status and its results are
- * not to be used. */
+/* Tests only: in this thread's next pa_weigh_tokens call, or pa_window_attend call
+ * whose kernel has waits (not the form for few rows), the device-side waits of number
+ * `wait` (0: none) give up at once, as they would after their limit: the call ends
+ * with PA_ERR_TIMEOUT in its status and its results are not to be used. */
 pa_status pa_session_fault(int32_t wait);
 
 /* Release a plan (NULL is ignored). */

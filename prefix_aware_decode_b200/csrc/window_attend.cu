@@ -90,7 +90,6 @@ struct AttendArgs {
   int lg;              // log2 G
   int slots, min_span, lanes;
   int whole;           // items are not cut: a CTA takes those that start in its span
-  int give_up;         // the wait (its code) that gives up at once; 0: none
   float scale_log2;
   uint16_t* out;
   float* lse;
@@ -205,13 +204,13 @@ struct Sums {
 };
 static_assert(sizeof(Sums) <= 5 * Shape<64>::TILE, "ring");
 
-// FAULT: the kernel of a call whose waits of one number give up (pa_session_fault); a
+// FAULT: the kernel of a call whose waits number give_up give up (pa_session_fault); a
 // comparison in every wait would cost all calls 3 %
 template <int D, bool FAULT>
 __global__ void __launch_bounds__(kThreads, 1)
     window_attend_kernel(const AttendArgs a, const __grid_constant__ CUtensorMap tq,
                          const __grid_constant__ CUtensorMap tq16, const __grid_constant__ CUtensorMap tk,
-                         const __grid_constant__ CUtensorMap tv) {
+                         const __grid_constant__ CUtensorMap tv, const int give_up) {
   using S = Shape<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023) {  // the swizzle needs it; the kernel has no other shared memory before it
@@ -340,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // is uniform (a loop that lanes leave one by one took 100 cycles).
   auto wwait = [&](uint64_t& b, int phase, int code) -> bool {
     const uint32_t ad = bar(b), par = (uint32_t)phase & 1u;
-    const bool quit = FAULT && code == a.give_up;
+    const bool quit = FAULT && code == give_up;
     if (!quit && __all_sync(0xffffffffu, mbar_try_wait(ad, par))) return true;
     const uint64_t t0 = global_timer_ns();
     while (quit || !__all_sync(0xffffffffu, mbar_try_wait(ad, par))) {
@@ -1065,10 +1064,10 @@ __global__ void __launch_bounds__(kShortThreads, 2) window_short_kernel(const At
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float y0 = see0 ? x[i] * a.scale_log2 : -INFINITY, y1 = see1 ? x[2 + i] * a.scale_log2 : -INFINITY;
-      float mx = max_nan(y0, y1);  // (a maximum that dropped NaN would leave such a row without keys)
+      float mx = fmaxf(y0, y1);  // (drops NaN: a row of NaN logits has no maximum, but weights and a sum of NaN)
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      mx = max_nan(mx, m[i]);
+      for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      mx = fmaxf(mx, m[i]);
       const float c = m[i] == mx ? 1.f : ex2(m[i] - mx);  // no key yet: 0, of nothing
       const float w0 = y0 == -INFINITY ? 0.f : ex2(y0 - mx), w1 = y1 == -INFINITY ? 0.f : ex2(y1 - mx);
       m[i] = mx;
@@ -1120,13 +1119,13 @@ __global__ void __launch_bounds__(kShortThreads, 2) window_short_kernel(const At
     float mx = -INFINITY, sum = 0.f;
     float2 o = make_float2(0.f, 0.f);
     auto add = [&](float t, float l1, float2 y) {
-      const float f = t == -INFINITY ? 0.f : ex2(t - mx);
+      const float f = l1 == 0.f ? 0.f : ex2(t - mx);  // a sum of 0: it saw nothing
       sum += f * l1;
       o.x += f * y.x;
       o.y += f * y.y;
     };
 #pragma unroll
-    for (int w = 0; w < kShortWarps; ++w) mx = max_nan(mx, top[w][h]);
+    for (int w = 0; w < kShortWarps; ++w) mx = fmaxf(mx, top[w][h]);
 #pragma unroll
     for (int w = 0; w < kShortWarps; ++w) add(top[w][h], sums[w][h], *reinterpret_cast<const float2*>(&part[w][h][d]));
     if (C == 1) {
@@ -1143,18 +1142,19 @@ __global__ void __launch_bounds__(kShortThreads, 2) window_short_kernel(const At
   cluster_sync();
   for (int i = 2 * (tid + kShortThreads * rank); i < G * D; i += 2 * kShortThreads * C) {
     const int h = i / D, d = i % D;
-    float t[kShortCluster], mx = -INFINITY, sum = 0.f;
+    float t[kShortCluster], l1[kShortCluster], mx = -INFINITY, sum = 0.f;
     float2 o = make_float2(0.f, 0.f);
 #pragma unroll
     for (int c = 0; c < kShortCluster; ++c) {
       t[c] = c < C ? cluster_read(&joined_top[h], c) : -INFINITY;
-      mx = max_nan(mx, t[c]);
+      l1[c] = c < C ? cluster_read(&joined_sum[h], c) : 0.f;
+      mx = fmaxf(mx, t[c]);
     }
 #pragma unroll
     for (int c = 0; c < kShortCluster; ++c) {
-      if (t[c] == -INFINITY) continue;  // it saw nothing
+      if (l1[c] == 0.f) continue;  // it saw nothing
       const float f = ex2(t[c] - mx);
-      sum += f * cluster_read(&joined_sum[h], c);
+      sum += f * l1[c];
       o.x += f * cluster_read(&joined[h][d], c);
       o.y += f * cluster_read(&joined[h][d + 1], c);
     }
@@ -1277,11 +1277,12 @@ bool launch_short(const pa::AttendArgs& a, int cluster, const void* q, const voi
 template <int D>
 bool launch(const pa::AttendArgs& a, const pa::Launch& l, const CUtensorMap& tq, const CUtensorMap& tq16,
             const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t cs) {
-  auto* k = a.give_up ? pa::window_attend_kernel<D, true> : pa::window_attend_kernel<D, false>;
+  const int give_up = pa_take_fault();
+  auto* k = give_up ? pa::window_attend_kernel<D, true> : pa::window_attend_kernel<D, false>;
   constexpr int smem = pa::Shape<D>::SMEM;
   static std::atomic<uint64_t> allowed[2];
-  if (!pa_allow_smem(k, smem, l.device, allowed[a.give_up ? 1 : 0])) return false;
-  if (!pa_launch_early(k, dim3(l.grid), dim3(pa::kThreads), smem, cs, 1, a, tq, tq16, tk, tv)) return false;
+  if (!pa_allow_smem(k, smem, l.device, allowed[give_up ? 1 : 0])) return false;
+  if (!pa_launch_early(k, dim3(l.grid), dim3(pa::kThreads), smem, cs, 1, a, tq, tq16, tk, tv, give_up)) return false;
   if (l.grid == l.lanes || a.whole) return true;  // no item is cut
   return pa_launch_early(pa::window_join_kernel<D>, dim3(l.grid - l.lanes, pa::kJoinY), dim3(256), 0, cs, 1, a);
 }
@@ -1314,7 +1315,6 @@ extern "C" pa_status pa_window_attend(const pa_sessions* b, int32_t window, int3
   a.slots = l.slots;
   a.min_span = l.min_span;
   a.whole = l.whole;
-  a.give_up = pa_take_fault();
   a.lanes = l.lanes;
   a.scale_log2 = (softmax_scale != 0.f ? softmax_scale : 1.f / sqrtf((float)b->head_dim)) * pa::kLog2e;
   a.out = static_cast<uint16_t*>(out);
