@@ -29,6 +29,17 @@ __device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
   return *reinterpret_cast<float2*>(&d);
 }
 
+// y minus the two bf16 numbers of a word (lower half first), in one mixed-precision step
+// each, which is exact where they are y rounded or cut to bf16.
+__device__ __forceinline__ float2 minus_bf16x2(float2 y, uint32_t w) {
+  float2 d;
+  asm("{\n .reg .b16 a, b, m;\n mov.b32 {a, b}, %2;\n mov.b16 m, 0xbf80;\n"
+      " fma.rn.f32.bf16 %0, a, m, %3;\n fma.rn.f32.bf16 %1, b, m, %4;\n}"
+      : "=f"(d.x), "=f"(d.y)
+      : "r"(w), "f"(y.x), "f"(y.y));
+  return d;
+}
+
 // After a wait gave up the barriers no longer tell what is in flight: 5 ms are
 // far more than any copy or product of this CTA can take to land.
 __device__ __forceinline__ void settle() {

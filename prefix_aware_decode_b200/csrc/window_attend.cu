@@ -26,9 +26,10 @@
 // Roles (384 threads): warps 0-3 and 4-7 softmax groups, one thread per row;
 // warp 8 issues the products; warp 9 walks the items and loads (TMA).  Per
 // block and tile: S = Q K^T (TMEM), P = exp2(S c - m c) written over S as P_hi + P_lo,
-// O += P V (TMEM).  P_hi is P cut to bf16, so that P - P_hi is exact in fp32, P_lo that
-// rest rounded to bf16: together within 2^-16 of P, as the planned decode's weights (one
-// bf16 alone is off by up to 2^-8 of a weight and left outputs 0.8 % off); l sums P.
+// O += P V (TMEM).  P_hi is P rounded or cut to bf16, so that P - P_hi is exact in fp32,
+// P_lo that rest rounded to bf16: together within 2^-16 of P, as the planned decode's
+// weights (one bf16 alone is off by up to 2^-8 of a weight and left outputs 0.8 % off); l
+// sums P.
 //   items of at most 64 rows   each row has two lanes of the tile (Q is loaded to both),
 //     16 rows to a warp's 32 lanes: one lane writes P_hi, the other P_lo, one product
 //     serves both and the epilogue adds the two
@@ -36,19 +37,20 @@
 // The running maximum is raised, and O rescaled, only when it grows by more than 2^8:
 // numerator and denominator use the same maximum, so the result is unchanged.
 //
-// Measured, with one bf16 | two products throughout | as it is: 64 windowed decodes 184,
-// 231, 195 us, a prompt chunk 2.0, 2.8, 2.75 ms, windowed chunks 42, 56, 51 us.  A block's
+// Measured, with one bf16 | two products throughout | as it is: 64 windowed decodes 179,
+// 225, 182 us, a prompt chunk 1.92, 2.8, 2.53 ms, windowed chunks 44, 56, 48 us.  A block's
 // weights are handed over at once: P_hi first (in 1, 2 or 4 parts) and P_lo while its
 // product runs: prompt chunk 2.8, 2.85, 3.4 ms, windowed chunks 54, 56, 65 us, for with
-// two tiles the product warp then waits where it could serve the other tile.
+// two tiles the product warp then waits where it could serve the other tile.  The rests
+// by masks and packed fp32 steps in place of mixed-precision ones: 199 us, 2.6 ms, 50 us.
 //
 // Bounds and measured device times, 32/8 heads of 128: decode rows by the bytes of
 // the visible cache and by how long a block's slots are held through its softmax (64
-// sessions, window 4096: 1.08 GB in 195 us captured back to back, 222 us issued one by
-// one; two of 100001-131072: 0.98 GB in 165-180 us); a prompt chunk of 4096 rows over
+// sessions, window 4096: 1.08 GB in 182 us, 5.9 TB/s; two of 100001-131072: 0.98 GB in
+// 160 us, 6.1 TB/s); a prompt chunk of 4096 rows over
 // 32768 tokens by the chain scores - softmax - product of a tile, two tiles being
-// all that tensor memory holds at 128 dims, and by power (2.45-2.85 ms, 0.72-0.84
-// PFLOP/s for the 1.5 times as many that the two parts of the weights take); a call of
+// all that tensor memory holds at 128 dims, and by power (2.45-2.6 ms, 0.79-0.84 PFLOP/s
+// of the definition's operations, 1.5 times as many done); a call of
 // one short item by its steps, about 11 us.
 #include <type_traits>
 
@@ -650,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int page_next = page_of(pair ? 0 : grp);
       float m = -INFINITY, l = 0.f;
       bool first = true;
-      // (two copies: in one the registers of both ways are live, prompt chunk 2.7 and 2.57 ms)
+      // (two copies; in one the registers of both ways are live: prompt chunk 2.57 -> 2.7 ms)
       auto walk = [&](auto twin_tag) {
         constexpr bool TWIN = decltype(twin_tag)::value;
         for (int j = pair ? 0 : grp; j < n && ok; j += pair ? 1 : 2) {
@@ -752,13 +754,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 sc = make_float2(a.scale_log2, a.scale_log2), mm = make_float2(mc, mc);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
           // the weights, 32 keys at a time
-          auto cut = [](float2 y) {  // to bf16
-            return make_float2(__uint_as_float(__float_as_uint(y.x) & 0xffff0000u),
-                               __uint_as_float(__float_as_uint(y.y) & 0xffff0000u));
-          };
-          const float2 neg = make_float2(-1.f, -1.f);
-          // of a row in two lanes: y cut, or what that leaves
-          const float2 fy = low ? make_float2(1.f, 1.f) : make_float2(0.f, 0.f), fc = low ? neg : make_float2(1.f, 1.f);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             float pw[32];
@@ -767,13 +762,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float2 z = ffma2(make_float2(x[c][i], x[c][i + 1]), sc, mm);
               const float2 y = make_float2(ex2(z.x), ex2(z.y));
               sum[(i >> 1) & 1] = fadd2(sum[(i >> 1) & 1], y);
-              if (TWIN) {
-                const float2 v = ffma2(cut(y), fc, fmul2(y, fy));
-                pw[i >> 1] = __uint_as_float(pack_bf16x2(v.x, v.y));
-              } else {  // of 16 keys 8 words P_hi, 8 words P_lo
-                const float2 v = ffma2(cut(y), neg, y);
+              if (TWIN) {  // (P_hi rounded; cut: 64 windowed decodes 188 and 182 us)
+                const uint32_t hi = pack_bf16x2(y.x, y.y);
+                const float2 v = minus_bf16x2(y, hi);
+                const uint32_t lo = pack_bf16x2(v.x, v.y);
+                pw[i >> 1] = __uint_as_float(low ? lo : hi);
+              } else {  // of 16 keys 8 words P_hi, cut, and 8 words P_lo
+                const uint32_t hi = __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x7632);
+                const float2 v = minus_bf16x2(y, hi);
                 const int w = (i & 16) + ((i & 15) >> 1);
-                pw[w] = __uint_as_float(__byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x7632));
+                pw[w] = __uint_as_float(hi);
                 pw[w + 8] = __uint_as_float(pack_bf16x2(v.x, v.y));
               }
             }
