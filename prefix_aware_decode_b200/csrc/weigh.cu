@@ -20,8 +20,8 @@
 // scores in 512 tensor cycles; so a part of them is computed on the FMA pipe
 // (kFmaPairs), which leaves both pipes about equally busy.  Measured, 32/8 heads of
 // 128: a decode step of 64 sessions of 2000-20000 tokens, 1.41 GB in 231-241 us (6.0
-// TB/s); chunks of 1500 and 2048 rows over 9000 and 16384 tokens, 361 GFLOP in 404
-// us (0.89 PFLOP/s; the exponential pipe 72% busy, 80% on the fullest SM).
+// TB/s); chunks of 1500 and 2048 rows over 9000 and 16384 tokens, 361 GFLOP in 405
+// us (0.89 PFLOP/s; the exponential pipe about 72% busy, 80% on the fullest SM).
 //
 // Roles (640 threads): warps 0-15 four groups of one thread per key, each with
 // its own score buffer in tensor memory; warp 16 issues the products; warp 17
@@ -42,8 +42,8 @@ constexpr int kThreads = 640;
 constexpr int kGroups = 1024;  // entries of the table of item prefixes
 constexpr int kQueue = 4;      // entries of the CTA's item queue
 // Of 16 pairs of scores: exponentials on the FMA pipe.  Prompt chunks (above) with
-// 0, 3, 4, 6: 451, 406, 404, 435 us.
-constexpr int kFmaPairs = 4;
+// 0, 3, 4, 6: 450, 405, 413, 431 us.
+constexpr int kFmaPairs = 3;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 // First failure of a device-side wait since pa_weigh_status last read it.

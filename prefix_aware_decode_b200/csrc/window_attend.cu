@@ -37,20 +37,22 @@
 // The running maximum is raised, and O rescaled, only when it grows by more than 2^8:
 // numerator and denominator use the same maximum, so the result is unchanged.
 //
-// Measured, with one bf16 | two products throughout | as it is: 64 windowed decodes 179,
-// 225, 182 us, a prompt chunk 1.92, 2.8, 2.53 ms, windowed chunks 44, 56, 48 us.  A block's
-// weights are handed over at once: P_hi first (in 1, 2 or 4 parts) and P_lo while its
-// product runs: prompt chunk 2.8, 2.85, 3.4 ms, windowed chunks 54, 56, 65 us, for with
-// two tiles the product warp then waits where it could serve the other tile.  The rests
-// by masks and packed fp32 steps in place of mixed-precision ones: 199 us, 2.6 ms, 50 us.
+// Measured: with one bf16 64 windowed decodes 178 us, windowed chunks 43 us, a prompt
+// chunk 1.92 ms; as it is 181 us, 47 us, 2.5 ms; with two products for few rows too 192
+// us, 64 decodes of 3000-4000 tokens 164 and not 155 us.  The rests by masks and packed
+// fp32 steps in place of mixed-precision ones: 199 us, 50 us, 2.6 ms.  Before that step,
+// weights handed over at once 2.75 ms and 51 us, P_hi first (in 1, 2 or 4 parts) and P_lo
+// while its product runs 2.8, 2.85, 3.4 ms and 54, 56, 65 us: with two tiles the product
+// warp then waits where it could serve the other one.
 //
 // Bounds and measured device times, 32/8 heads of 128: decode rows by the bytes of
 // the visible cache and by how long a block's slots are held through its softmax (64
-// sessions, window 4096: 1.08 GB in 182 us, 5.9 TB/s; two of 100001-131072: 0.98 GB in
+// sessions, window 4096: 1.08 GB in 181 us, 6.0 TB/s; two of 100001-131072: 0.98 GB in
 // 160 us, 6.1 TB/s); a prompt chunk of 4096 rows over
 // 32768 tokens by the chain scores - softmax - product of a tile, two tiles being
-// all that tensor memory holds at 128 dims, and by power (2.45-2.6 ms, 0.79-0.84 PFLOP/s
-// of the definition's operations, 1.5 times as many done); a call of
+// all that tensor memory holds at 128 dims, and by power (2.25 ms alone, 2.5-2.6 ms in a
+// loop, 0.79-0.92 PFLOP/s of the definition's operations, 1.5 times as many done; tensor
+// pipe 76%, exponential pipe 51% busy); a call of
 // one short item by its steps, about 11 us.
 #include <type_traits>
 
@@ -67,11 +69,11 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kThreads = 384;
 constexpr int kMaxChunks = 256;      // chunks of kThreads tile slots that a CTA sums
 constexpr int kQueue = 2;            // entries of the CTA's item queue
-// items of at most so many blocks are not cut: 8 windowed chunks of 1-700 rows 42 us,
-// all items cut 50 us; whole up to 32 blocks: 4 sessions of 4096, 3 rows, 38 and 26 us
+// items of at most so many blocks are not cut: 8 windowed chunks of 1-700 rows 47 us,
+// all items cut 55 us; whole up to 32 blocks: 4 sessions of 4096, 3 rows, 46 and 28 us
 constexpr int kWholeBlocks = 8;
 // most kv heads walked side by side (148 SMs = 37 spans of 4); 1: 64 windowed decodes
-// 183.6 and 179.8 us, 64 of 300-1000 with 5 rows 58.8 and 52.9 us
+// 204 and 180 us, 64 of 300-1000 with 5 rows 67 and 60 us
 constexpr int kLanes = 4;
 constexpr int kTwinRows = 64;        // most rows of an item that has each in two lanes
 constexpr float kRaise = 8.f;        // log2 growth of a maximum that raises it
@@ -890,8 +892,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // item cut at the start of the span after CTA c's, when that is its first cut.
 // A warp per row; when there are few rows and many parts the block's eight warps
 // per row, each every eighth part (the sum is kept in that order on every run).
-// One session of 60000 tokens, 8 heads of 1 kv head, whole call: 1 row 47 -> 20 us,
-// 4 rows 47 -> 21.5 us, 8 rows 66 -> 28 us.  32 blocks an item (most find nothing
+// One session of 60000 tokens, 8 heads of 1 kv head, whole call: 1 row 21 us, 4 rows 23
+// us, 8 rows 28 us (a warp a row and 8 blocks an item throughout: 47, 47, 66 us).  32 blocks an item (most find nothing
 // to do) cost other calls nothing measurable against 8.
 constexpr int kJoinY = 32;
 template <int D>
