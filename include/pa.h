@@ -381,15 +381,16 @@ pa_status pa_attend_noalloc(const pa_plan *plan, const void *q, const void *k_po
  * The i-th of the n rows of a session is its cached token kv_len - n + i (its
  * position).  A block-table entry outside [0, num_pages_in_pool) is a hole: its
  * tokens are neither written, seen nor copied (pa_evict_tokens says what it does
- * when it keeps one).  The K and V of tokens that some
- * row sees are finite; other tokens and slots may hold anything, NaN included.
- * The device arrays are read when the kernels run.  Arguments are checked
- * before anything is enqueued: PA_ERR_INVALID for a null or misaligned pointer
+ * when it keeps one).  The K and V of tokens that some row sees are finite; other
+ * tokens and slots may hold anything, NaN included.  The device arrays are read
+ * when the kernels run.  Forms of the kernels are chosen by max_pages, not by the
+ * lengths: a table no wider than its sessions need is the faster one.  Arguments
+ * are checked before anything is enqueued: PA_ERR_INVALID for a null or misaligned pointer
  * (q, k, v, pools, outputs: 16 bytes) or a bad size, PA_ERR_UNSUPPORTED for a
  * head layout, head_dim or page size that is not built, a pool beyond 2^31 - 1
- * (page, head, slot) rows, or more than 98304 tiles (num_rows / (256 / G) + S), PA_ERR_CUDA when a launch fails.  All are asynchronous on
- * `stream` of the current device, keep nothing between calls and are bit
- * reproducible.
+ * (page, head, slot) rows, or more than 98304 tiles (num_rows / (256 / G) + S),
+ * PA_ERR_CUDA when a launch fails.  All are asynchronous on `stream` of the current
+ * device, keep nothing between calls and are bit reproducible.
  */
 typedef struct {
   int32_t n_sessions, num_rows;

@@ -5,7 +5,9 @@ window and sinks, accumulated attention weights, and eviction.
 Every call takes the sessions' block table [S][max_pages], cached lengths [S]
 and row offsets [S + 1] as int32 CUDA tensors and reads them when its kernels
 run: nothing is planned on the host or copied back, so a call can be captured
-into a CUDA graph and replayed as the lengths and tables change in place.
+into a CUDA graph and replayed as the lengths and tables change in place.  Kernels
+are chosen by the table's width, which bounds the lengths: a table no wider than the
+steps need is the faster one.
 
 All tensors of a call live on one device, which need not be the current one.
 A call runs on `stream` (a torch stream of that device, or a cudaStream_t), or on

@@ -958,20 +958,21 @@ __global__ void __launch_bounds__(256) window_join_kernel(const AttendArgs a) {
 // piece serves two products); the weights stay in fp32; P V on the CUDA cores; the
 // warps' results are joined in shared memory, the CTAs' through the cluster's.
 //
-// Taken for two rows a session on average and up to 128 pages a CTA, 64 and 32
-// for groups of 4 and 8, whose P V costs more.  Measured, this form against the
-// other (device time of a call; query / kv heads x dims):
-//   1 x 20 tokens, 8/8x64           2.7   12.1 us    64 x 300-900, 8/1x128        12.8  16.8 us
-//   4 x 300, 8/2x64                 4.6   10.4       8 x 500-1000, 32/4x128       12.9  16.0
-//   4 x 1500-2000, 32/8x128        11.6   19.4       2 x 900-1000, 64/8x64         6.9  14.3
-//   1 x 6000-8000, 32/8x128        19.9   22.0       1 x 12000-16000, 8/8x128     24.5  26.2
-//   64 x 500-1000, 32/8x128        44.4   52.5       64 x 1500-2000, 8/8x64       45.0  67.8
-//   256 x 400-900, 32/8x128       124.3  149.3       256 x 1200-1900, 8/4x128    132.6 143.5 (6.1 TB/s)
-// Past the rule the other wins: 64 x 1500-2000, 32/8x128: 89.5 and 85.7 us; 64 x
-// 3000-4000: 169 and 153 us; 256 x 100-900, 64/8x128: 142.8 and 137.3 us; 4 rows a
-// session, each a read of the same pages, 16 x 500-900: 39.6 and 23.8 us.  The rows are
-// counted on average, since the host does not know them one by one: a chunk of 64 rows
-// over 800 tokens among 63 single rows, 32/8x128: 54.5 and 51.6 us.
+// Taken for two rows a session on average and up to 128 pages a CTA (of the table's
+// width, or what a window leaves of it), 64 and 32 for groups of 4 and 8, whose P V costs
+// more.  Measured, this form against the other (device time of a call; query / kv heads x
+// dims):
+//   1 x 20 tokens, 8/8x64           2.7   13.8 us    64 x 300-900, 8/1x128        12.6  18.9 us
+//   4 x 300, 8/2x64                 4.5   11.8       8 x 500-1000, 32/4x128        9.5  18.0
+//   4 x 1500-2000, 32/8x128        10.8   21.8       2 x 900-1000, 64/8x64         6.8  16.7
+//   1 x 6000-8000, 32/8x128        18.5   23.2       1 x 12000-16000, 8/8x128     24.4  26.3
+//   64 x 500-1000, 32/8x128        44.3   59.6       64 x 1500-2000, 8/8x64       45.0  83.5
+//   256 x 400-900, 32/8x128       124.0  173.9       256 x 1200-1900, 8/4x128    130.0 149.8 (6.1 TB/s)
+// Past the rule: 64 x 1500-2000, 32/8x128: 89.5 and 91.3 us; 64 x 3000-4000: 169 and 155
+// us; 256 x 100-900, 64/8x128: 143 and 157 us; 4 rows a session, each a read of the same
+// pages, 16 x 500-900: 39.6 and 26.7 us.  The rows are counted on average, since the host
+// does not know them one by one: a chunk of 64 rows over 800 tokens among 63 single rows,
+// 32/8x128: 52.0 and 49.4 us; of 256 over 1000 among 255: 209 and 187 us.
 constexpr int kShortPages = 128;
 constexpr int kShortCluster = 8;
 constexpr int kShortThreads = 256, kShortWarps = kShortThreads / 32;
