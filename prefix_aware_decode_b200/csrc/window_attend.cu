@@ -1299,9 +1299,7 @@ extern "C" pa_status pa_window_attend(const pa_sessions* b, int32_t window, int3
   pa::Launch l;
   if (!pa::plan_launch(*b, pa_window(window, sinks), &l)) return PA_ERR_UNSUPPORTED;
   if (b->num_rows == 0) {  // nothing but the status of a workspace that is given
-    if (!d_workspace) return PA_OK;
-    if (reinterpret_cast<uintptr_t>(d_workspace) & 255) return PA_ERR_INVALID;
-    if (workspace_bytes < l.bytes) return PA_ERR_NOMEM;
+    if (!d_workspace || (reinterpret_cast<uintptr_t>(d_workspace) & 255) || workspace_bytes < 4) return PA_OK;
     return cudaMemsetAsync(d_workspace, 0, 4, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
   }
   if (!q || !k_pool || !v_pool || !out || !d_workspace) return PA_ERR_INVALID;

@@ -255,6 +255,9 @@ def test_window_status_of_calls_that_do_nothing():
     assert ref.pad.window_status(ws) == ref.pad.PA_OK
     fresh = ref.pad.window_workspace(q, k, table, lens, cu)
     assert ref.pad.window_status(fresh) == ref.pad.PA_OK
+    small = torch.full((256,), 255, dtype=torch.uint8, device="cuda")  # nothing is done: any workspace will do
+    ref.pad.window_attend(q, k, v, table, lens, cu, workspace=small)
+    assert ref.pad.window_status(small) == ref.pad.PA_OK
 
 
 @gpu
