@@ -28,7 +28,7 @@
 // block and tile: S = Q K^T (TMEM), P = exp2(S c - m c) written over S as P_hi + P_lo,
 // O += P V (TMEM).  P_hi is P rounded or cut to bf16, so that P - P_hi is exact in fp32,
 // P_lo that rest rounded to bf16: together within 2^-16 of P, as the planned decode's
-// weights (one bf16 alone is off by up to 2^-8 of a weight and left outputs 0.8 % off); l
+// weights (one bf16 alone is off by up to 2^-8 of a weight, up to 0.9 % of an output); l
 // sums P.
 //   items of at most 64 rows   each row has two lanes of the tile (Q is loaded to both),
 //     16 rows to a warp's 32 lanes: one lane writes P_hi, the other P_lo, one product
@@ -48,12 +48,11 @@
 // Bounds and measured device times, 32/8 heads of 128: decode rows by the bytes of
 // the visible cache and by how long a block's slots are held through its softmax (64
 // sessions, window 4096: 1.08 GB in 181 us, 6.0 TB/s; two of 100001-131072: 0.98 GB in
-// 160 us, 6.1 TB/s); a prompt chunk of 4096 rows over
-// 32768 tokens by the chain scores - softmax - product of a tile, two tiles being
-// all that tensor memory holds at 128 dims, and by power (2.25 ms alone, 2.5-2.6 ms in a
-// loop, 0.79-0.92 PFLOP/s of the definition's operations, 1.5 times as many done; tensor
-// pipe 76%, exponential pipe 51% busy); a call of
-// one short item by its steps, about 11 us.
+// 160 us, 6.1 TB/s); a prompt chunk of 4096 rows over 32768 tokens by the chain scores -
+// softmax - product of a tile, two tiles being all that tensor memory holds at 128 dims,
+// and by power (2.25 ms alone, 2.5-2.6 ms in a loop, 0.79-0.92 PFLOP/s of the definition's
+// operations, 1.5 times as many done; tensor pipe 76%, exponential pipe 51% busy); a call
+// of one short item by its steps, about 12 us.
 #include <type_traits>
 
 #include "ptx.cuh"
